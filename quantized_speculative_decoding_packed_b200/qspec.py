@@ -371,6 +371,20 @@ def attn_workspace_size(batch: int, t_new: int, h_q: int, h_kv: int, ctx_max: in
     return int(LIB.qspec_attn_workspace_size(batch, t_new, h_q, h_kv, HEAD_DIM, ctx_max))
 
 
+# attn_decode's default workspaces, by device and number of arrival counters: the partial
+# results behind the counters lie where the GEMMs keep their split-tile tickets, and where
+# a call with more counters has counters, which must both be zero.
+_ATTN_WS_CACHE: dict = {}
+
+
+def _attn_workspace(nbytes: int, device: torch.device, counters: int) -> torch.Tensor:
+    cur = _ATTN_WS_CACHE.get((device, counters))
+    if cur is None or cur.numel() < nbytes:
+        cur = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _ATTN_WS_CACHE[(device, counters)] = cur
+    return cur
+
+
 def kv_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor,
               v_cache: torch.Tensor, h_q: int, work: torch.Tensor | None = None, stream=None):
     """Write the new tokens' keys and values (rows b*T + t of the fused QKV output)
@@ -396,7 +410,7 @@ def attn_decode(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: tor
     if out is None:
         out = torch.empty((b * t_new, h_q * HEAD_DIM), dtype=torch.float32, device=qkv.device)
     if work is None:
-        work = workspace(attn_workspace_size(b, t_new, h_q, h_kv, ctx_max), qkv.device)
+        work = _attn_workspace(attn_workspace_size(b, t_new, h_q, h_kv, ctx_max), qkv.device, b * h_kv)
     _check(LIB.qspec_attn_decode(_ptr(qkv), qkv.stride(0), b, t_new, h_q, h_kv, HEAD_DIM,
                                  _ptr(lens), offset, _ptr(k_cache), _ptr(v_cache), l_max, ctx_max,
                                  _ptr(out), out.stride(0), _ptr(work), work.numel(),
