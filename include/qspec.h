@@ -337,6 +337,95 @@ qspec_status qspec_kv_commit(int32_t* lens, const int32_t* n_accepted, int32_t b
                              int32_t l_max, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The prompt path over the same cache: positions, prompts, shared prefixes.
+ * Tokens are packed: row i of `qkv`, `q` and `out` is packed token i.  With
+ * `cu` (device int32 [batch + 1], cu[0] = 0, not decreasing, cu[batch] <= n_tokens)
+ * sequence b has the tokens cu[b] .. cu[b+1]-1, possibly none; rows from
+ * cu[batch] on are padding: not read for any result, never written.  With cu
+ * NULL (where allowed) every sequence has n_tokens / batch of them.  Token i
+ * of sequence b (from 0) is at position lens[b] + offset + i of its cache; a
+ * packed prompt is committed with n_accepted[b] = (its tokens) - 1.
+ * Requires head_dim = 128, h_q a multiple of h_kv, 1 <= batch <= 65535,
+ * n_tokens >= 1.  All reads of device-side lengths are checked: a sequence
+ * whose cu entries or positions do not fit is skipped (its output rows zero)
+ * and reported as QSPEC_ERR_BAD_INPUT through qspec_workspace_status.
+ * Asynchronous on `stream`; launched as programmatic dependents of the
+ * preceding kernel, which they wait for before they read or write anything.
+ */
+
+/* Angles for qspec_qkv_rope_append: table[p][i] = cos(p * inv_freq[i]),
+ * table[p][rot/2 + i] = sin(p * inv_freq[i]) for p < positions, i < rot/2,
+ * computed in 64 bits and rounded once.
+ *  inv_freq   [rot/2] fp64 (device); table [positions][rot] fp32 out.
+ * Requires rot a multiple of 8 in [8, 128], 1 <= positions < 2^31. */
+qspec_status qspec_rope_table(const double* inv_freq, int32_t rot, int64_t positions, float* table, void* stream);
+
+/* Norms, rotation and cache append of a fused QKV projection (rows as for
+ * qspec_kv_append).  Each query head x (and key head, with k_gamma):
+ *   x <- x / sqrt(mean(x^2) + eps) * gamma       if its gamma is not NULL,
+ *   (x_i, x_k) <- (x_i c - x_k s, x_k c + x_i s) for the pairs (i, i + rot/2), i < rot/2,
+ *                                                 or (2i, 2i + 1) with QSPEC_ROPE_INTERLEAVED,
+ * with c, s from row (*prefix_len + lens[b] + offset + t) of `table`.  Keys and
+ * values are rounded to bf16 (nearest even) into the cache at lens[b] + offset + t;
+ * the values are not turned.  fp32 arithmetic.
+ *  q_gamma, k_gamma  fp32 [128], each may be NULL (no norm).
+ *  table      as qspec_rope_table writes it, `positions` rows; rot = 0: no rotation (table NULL).
+ *  prefix_len device int32 [1] or NULL (0): tokens of a shared prefix before every sequence.
+ *  q_out      the queries: bf16 [n_tokens][ld_q], or fp32 with QSPEC_ROPE_Q_FP32.  fp32 queries may be
+ *             turned in place (q_out = qkv, ld_q = ld_qkv): the rows are then what qspec_attn_decode
+ *             takes.  No other overlap.
+ *  workspace  optional (NULL, or >= 256 zeroed bytes): the status word.  A token whose position is
+ *             outside the cache or the table writes nothing and is reported there.
+ * Requires rot a multiple of 8 in [0, 128], ld_qkv >= (h_q + 2 h_kv) * 128 and a multiple of 4,
+ * ld_q >= h_q * 128 and a multiple of 8 (fp32: 4). */
+#define QSPEC_ROPE_INTERLEAVED 1u
+#define QSPEC_ROPE_Q_FP32 2u
+qspec_status qspec_qkv_rope_append(const float* qkv, int64_t ld_qkv, int64_t n_tokens, int32_t batch,
+                                   const int32_t* cu, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                                   const float* q_gamma, const float* k_gamma, float eps, const float* table,
+                                   int64_t positions, int32_t rot, const int32_t* prefix_len, const int32_t* lens,
+                                   int32_t offset, uint16_t* k_cache, uint16_t* v_cache, int32_t l_max, void* q_out,
+                                   int64_t ld_q, uint32_t flags, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Causal attention of packed prompts over the cache (call after the tokens'
+ * keys and values are in it): token i of sequence b sees positions
+ * 0 .. lens[b] + i,  out = sum_j w_j v_j,  w = softmax_j(q . k_j / sqrt(128)).
+ *  q          bf16 [n_tokens][ld_q], head h at column h * 128 (as qspec_qkv_rope_append writes it).
+ *  out        bf16 [n_tokens][ld_out]: what qspec_gemm_w4a16 takes.  Must not overlap q.
+ *  workspace  >= qspec_attn_prefill_workspace_size() bytes, 16-byte aligned; its first 4 bytes zero
+ *             before the first use.  Calls sharing one workspace must not overlap.
+ * Scores, softmax statistics and sums in fp32; the softmax weights are rounded to bf16 before they meet
+ * the bf16 values.  What is stored past the last position that a sequence sees does not matter, not even NaN.
+ * Requires h_q / h_kv <= 128, ld_q and ld_out >= h_q * 128 and multiples of 8. */
+qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
+                                int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens,
+                                const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max, uint16_t* out,
+                                int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of a batch whose sequences share one prefix: token t of sequence b
+ * sees the *prefix_len positions of the prefix and positions 0 .. lens[b] + offset + t
+ * of its own cache, under one softmax.  The prefix is read once for the tokens of
+ * all sequences together.
+ *  prefix_k, prefix_v  bf16 [h_kv][prefix_max][128] (a cache of batch 1, filled like any other).
+ *  prefix_len  device int32 [1], 0 .. prefix_max; otherwise every output row is zero and
+ *              QSPEC_ERR_BAD_INPUT is reported.
+ *  cu          NULL: the drafting and verifying passes (n_tokens / batch tokens for each sequence);
+ *              else packed prompts behind the prefix.
+ *  workspace   >= qspec_attn_prefix_workspace_size(...) bytes.
+ * Otherwise as qspec_attn_prefill. */
+qspec_status qspec_attn_prefix(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
+                               int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens, int32_t offset,
+                               const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max,
+                               const uint16_t* prefix_k, const uint16_t* prefix_v, int32_t prefix_max,
+                               const int32_t* prefix_len, uint16_t* out, int64_t ld_out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace on the current device (0: invalid arguments or device). */
+size_t qspec_attn_prefill_workspace_size(void);
+size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q);
+
+/*
  * W4A16 verifying GEMM that allocates nothing and takes no workspace.
  * The pages have no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory at the point of the call: a plugin

@@ -14,6 +14,8 @@
 #include "accept.cuh"
 #include "attention.cuh"
 #include "gemm.cuh"
+#include "prompt_attention.cuh"
+#include "prompt_rope.cuh"
 #include "qspec.h"
 #include "quantize.cuh"
 
@@ -96,6 +98,19 @@ bool make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem, const v
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 tensor of up to 4 dimensions, innermost first; strides in bytes from dimension 1 on;
+// 128-byte swizzled tiles.
+template <int kDims>
+bool make_tmap_bf16(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[kDims],
+                    const cuuint64_t (&strides)[kDims - 1], const cuuint32_t (&box)[kDims]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDims, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -368,6 +383,131 @@ qspec_status run_gemm(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return QSPEC_ERR_CUDA;
   return launch_qgemm<kInt8>(p.mt, fused, tw, tx, ts, a, p.grid, dev, stream);
+}
+
+// ---------------------------------------------------------------- the prompt path
+// A kernel as a programmatic dependent of the one before it on the stream.
+template <typename... P, typename... A>
+qspec_status launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, void* stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return QSPEC_ERR_CUDA;
+  }
+  return QSPEC_OK;
+}
+
+// Shapes of the calls on packed tokens; cu == NULL: n_tok / batch tokens for every sequence.
+bool packed_shape_ok(int64_t n_tok, int32_t batch, bool packed, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                     int32_t l_max, int32_t offset) {
+  if (batch < 1 || batch > 65535 || n_tok < 1 || n_tok > 0x7FFFFFFFll - 256) return false;
+  if (h_q < 1 || h_kv < 1 || h_kv > 65535 || head_dim != kHeadDim || (h_q % h_kv) != 0) return false;
+  if (h_q > (1 << 20) || l_max < 1 || l_max > 0x7FFFFFFF - 256 || offset < 0) return false;
+  if (!packed && (n_tok % batch) != 0) return false;
+  return static_cast<int64_t>(batch) * h_kv <= 0x7FFFFFFFll;
+}
+
+// Whether [p, p + bytes) and [q, q + other) have a byte in common.
+bool overlap(const void* p, int64_t bytes, const void* q, int64_t other) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + static_cast<uintptr_t>(other) && b < a + static_cast<uintptr_t>(bytes);
+}
+
+// [heads][rows][128] bf16 as tiles of 128 rows: the two 64-column halves of a tile one after the other.
+bool make_kv_tmap(CUtensorMap* map, const uint16_t* base, uint64_t heads, uint64_t rows) {
+  const cuuint64_t dims[4] = {64, rows, 2, heads};
+  const cuuint64_t strides[3] = {kHeadDim * 2, 128, rows * kHeadDim * 2};
+  const cuuint32_t box[4] = {64, 128, 2, 1};
+  return make_tmap_bf16<4>(map, base, dims, strides, box);
+}
+
+// The attention of many tokens, with or without a shared prefix.
+qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok, int32_t batch, const int32_t* cu,
+                                  int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens, int32_t offset,
+                                  const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max, bool with_prefix,
+                                  const uint16_t* prefix_k, const uint16_t* prefix_v, int32_t prefix_max,
+                                  const int32_t* prefix_len, uint16_t* out, int64_t ld_out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!q || !lens || !k_cache || !v_cache || !out || !workspace) return QSPEC_ERR_INVALID_ARG;
+  if (with_prefix && (!prefix_k || !prefix_v || !prefix_len || prefix_max < 1 || prefix_max > 0x7FFFFFFF - 256))
+    return QSPEC_ERR_INVALID_ARG;
+  if (!packed_shape_ok(n_tok, batch, cu != nullptr, h_q, h_kv, head_dim, l_max, offset)) return QSPEC_ERR_INVALID_ARG;
+  const int32_t group = h_q / h_kv;
+  const int64_t cols = static_cast<int64_t>(h_q) * kHeadDim;
+  if (group > 128 || n_tok * h_q > (1ll << 33)) return QSPEC_ERR_INVALID_ARG;
+  if (ld_q < cols || (ld_q % 8) != 0 || ld_q >= (1ll << 38) || ld_out < cols || (ld_out % 8) != 0 ||
+      ld_out > (1ll << 40) / n_tok || ld_q > (1ll << 40) / n_tok)
+    return QSPEC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lens, 4) ||
+      !aligned(cu, 4) || !aligned(prefix_len, 4) || !aligned(prefix_k, 16) || !aligned(prefix_v, 16) ||
+      !aligned(workspace, 16))
+    return QSPEC_ERR_INVALID_ARG;
+  if (overlap(q, ((n_tok - 1) * ld_q + cols) * 2, out, ((n_tok - 1) * ld_out + cols) * 2)) return QSPEC_ERR_INVALID_ARG;
+  int dev = 0;
+  DeviceInfo info;
+  qspec_status st = current_device(&dev, &info);
+  if (st != QSPEC_OK) return st;
+  const int grid = info.sm_count;
+  const PaLayout lay = pa_layout(grid, batch, n_tok * h_q, with_prefix);
+  if (workspace_bytes < static_cast<size_t>(lay.total)) return QSPEC_ERR_WORKSPACE_TOO_SMALL;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPaSmemBytes) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return QSPEC_ERR_CUDA;
+    }
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  PromptArgs a;
+  a.cu = cu;
+  a.lens = lens;
+  a.prefix_len = with_prefix ? prefix_len : nullptr;
+  a.out = out;
+  a.work = static_cast<uint8_t*>(workspace);
+  a.ld_out = ld_out;
+  a.off_start = lay.off_start;
+  a.off_desc = lay.off_desc;
+  a.off_ml = lay.off_ml;
+  a.off_o = lay.off_o;
+  a.off_row_ml = lay.off_row_ml;
+  a.off_row_o = lay.off_row_o;
+  a.n_tok = static_cast<int>(n_tok);
+  a.batch = batch;
+  a.t_new = cu ? 0 : static_cast<int>(n_tok / batch);
+  a.offset = offset;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.group = group;
+  a.tpt = 128 / group;
+  a.l_max = l_max;
+  a.prefix_max = with_prefix ? prefix_max : 0;
+  CUtensorMap tq, tk, tv, tpk, tpv;
+  const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
+  const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};
+  const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(a.tpt)};
+  const uint64_t heads = static_cast<uint64_t>(batch) * h_kv;
+  if (!make_tmap_bf16<3>(&tq, q, q_dims, q_strides, q_box) || !make_kv_tmap(&tk, k_cache, heads, l_max) ||
+      !make_kv_tmap(&tv, v_cache, heads, l_max))
+    return QSPEC_ERR_CUDA;
+  tpk = tk;
+  tpv = tv;
+  if (with_prefix && (!make_kv_tmap(&tpk, prefix_k, h_kv, prefix_max) || !make_kv_tmap(&tpv, prefix_v, h_kv, prefix_max)))
+    return QSPEC_ERR_CUDA;
+  st = launch_dependent(prompt_attention_kernel, dim3(static_cast<unsigned>(grid)), kPaThreads, kPaSmemBytes, stream,
+                        tq, tk, tv, tpk, tpv, a);
+  if (st != QSPEC_OK) return st;
+  if (!with_prefix) return launch_dependent(prompt_join_kernel, dim3(static_cast<unsigned>(grid), 8), 256, 0, stream, a);
+  return launch_dependent(prefix_join_kernel, dim3(static_cast<unsigned>((n_tok * h_q + 7) / 8)), 256, 0, stream, a);
 }
 
 }  // namespace
@@ -645,6 +785,117 @@ qspec_status qspec_kv_commit(int32_t* lens, const int32_t* n_accepted, int32_t b
                      static_cast<cudaStream_t>(stream)>>>(lens, n_accepted, batch, l_max,
                                                           static_cast<uint32_t*>(workspace));
   return cudaGetLastError() == cudaSuccess ? QSPEC_OK : QSPEC_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- the prompt path
+qspec_status qspec_rope_table(const double* inv_freq, int32_t rot, int64_t positions, float* table, void* stream) {
+  if (!inv_freq || !table) return QSPEC_ERR_INVALID_ARG;
+  if (rot < 8 || rot > kHeadDim || (rot % 8) != 0 || positions < 1 || positions > 0x7FFFFFFFll)
+    return QSPEC_ERR_INVALID_ARG;
+  if (!aligned(inv_freq, 8) || !aligned(table, 16)) return QSPEC_ERR_INVALID_ARG;
+  qspec_status st = current_device(nullptr, nullptr);
+  if (st != QSPEC_OK) return st;
+  const int64_t blocks = (positions * (rot / 2) + 255) / 256;
+  rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      inv_freq, positions, rot / 2, table);
+  return cudaGetLastError() == cudaSuccess ? QSPEC_OK : QSPEC_ERR_CUDA;
+}
+
+qspec_status qspec_qkv_rope_append(const float* qkv, int64_t ld_qkv, int64_t n_tokens, int32_t batch,
+                                   const int32_t* cu, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                                   const float* q_gamma, const float* k_gamma, float eps, const float* table,
+                                   int64_t positions, int32_t rot, const int32_t* prefix_len, const int32_t* lens,
+                                   int32_t offset, uint16_t* k_cache, uint16_t* v_cache, int32_t l_max, void* q_out,
+                                   int64_t ld_q, uint32_t flags, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (!qkv || !lens || !k_cache || !v_cache || !q_out) return QSPEC_ERR_INVALID_ARG;
+  if (!packed_shape_ok(n_tokens, batch, cu != nullptr, h_q, h_kv, head_dim, l_max, offset)) return QSPEC_ERR_INVALID_ARG;
+  if ((flags & ~(QSPEC_ROPE_INTERLEAVED | QSPEC_ROPE_Q_FP32)) != 0u) return QSPEC_ERR_INVALID_ARG;
+  if (rot < 0 || rot > kHeadDim || (rot % 8) != 0 || (rot > 0 && (!table || positions < 1))) return QSPEC_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !(eps < 1e30f)) return QSPEC_ERR_INVALID_ARG;
+  const int64_t cols = static_cast<int64_t>(h_q) * kHeadDim;
+  const int64_t all = static_cast<int64_t>(h_q + 2 * h_kv) * kHeadDim;
+  const bool q32 = (flags & QSPEC_ROPE_Q_FP32) != 0u;
+  if (ld_qkv < all || (ld_qkv % 4) != 0 || ld_qkv > (1ll << 40) / n_tokens || ld_q < cols ||
+      (ld_q % (q32 ? 4 : 8)) != 0 || ld_q > (1ll << 40) / n_tokens)
+    return QSPEC_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(lens, 4) || !aligned(cu, 4) || !aligned(prefix_len, 4) || !aligned(q_gamma, 16) ||
+      !aligned(k_gamma, 16) || !aligned(table, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(q_out, 16))
+    return QSPEC_ERR_INVALID_ARG;
+  // the queries may be turned in place, nothing else of the projection may be written over
+  const bool in_place = q32 && q_out == qkv && ld_q == ld_qkv;
+  if (!in_place &&
+      overlap(qkv, ((n_tokens - 1) * ld_qkv + all) * 4, q_out, ((n_tokens - 1) * ld_q + cols) * (q32 ? 4 : 2)))
+    return QSPEC_ERR_INVALID_ARG;
+  if (workspace && (workspace_bytes < 256 || !aligned(workspace, 16))) return QSPEC_ERR_INVALID_ARG;
+  const int64_t slices = (h_q + 2 * h_kv + kRopeHeadsPerCta - 1) / kRopeHeadsPerCta;
+  if (slices > 65535) return QSPEC_ERR_INVALID_ARG;
+  qspec_status st = current_device(nullptr, nullptr);
+  if (st != QSPEC_OK) return st;
+  RopeArgs a;
+  a.qkv = qkv;
+  a.cu = cu;
+  a.lens = lens;
+  a.prefix_len = prefix_len;
+  a.q_gamma = q_gamma;
+  a.k_gamma = k_gamma;
+  a.table = table;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.q_out = q_out;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.ld = ld_qkv;
+  a.ld_q = ld_q;
+  a.table_rows = positions;
+  a.eps = eps;
+  a.n_tok = static_cast<int>(n_tokens);
+  a.batch = batch;
+  a.t_new = cu ? 0 : static_cast<int>(n_tokens / batch);
+  a.offset = offset;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.rot = rot;
+  a.l_max = l_max;
+  a.interleaved = (flags & QSPEC_ROPE_INTERLEAVED) ? 1 : 0;
+  a.q_f32 = q32 ? 1 : 0;
+  return launch_dependent(qkv_rope_append_kernel, dim3(static_cast<unsigned>(n_tokens), static_cast<unsigned>(slices)),
+                          kRopeWarps * 32, 0, stream, a);
+}
+
+size_t qspec_attn_prefill_workspace_size(void) {
+  DeviceInfo info;
+  if (current_device(nullptr, &info) != QSPEC_OK) return 0;
+  return static_cast<size_t>(pa_layout(info.sm_count, 0, 0, false).total);
+}
+
+size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q) {
+  if (n_tokens < 1 || n_tokens > 0x7FFFFFFFll - 256 || batch < 1 || batch > 65535 || h_q < 1 || h_q > (1 << 20) ||
+      n_tokens * h_q > (1ll << 33))
+    return 0;
+  DeviceInfo info;
+  if (current_device(nullptr, &info) != QSPEC_OK) return 0;
+  return static_cast<size_t>(pa_layout(info.sm_count, batch, n_tokens * h_q, true).total);
+}
+
+qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
+                                int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens,
+                                const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max, uint16_t* out,
+                                int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cu) return QSPEC_ERR_INVALID_ARG;
+  return run_prompt_attention(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, 0, k_cache, v_cache, l_max,
+                              false, nullptr, nullptr, 0, nullptr, out, ld_out, workspace, workspace_bytes, stream);
+}
+
+qspec_status qspec_attn_prefix(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
+                               int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens, int32_t offset,
+                               const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max,
+                               const uint16_t* prefix_k, const uint16_t* prefix_v, int32_t prefix_max,
+                               const int32_t* prefix_len, uint16_t* out, int64_t ld_out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_prompt_attention(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, offset, k_cache, v_cache, l_max,
+                              true, prefix_k, prefix_v, prefix_max, prefix_len, out, ld_out, workspace,
+                              workspace_bytes, stream);
 }
 
 size_t qspec_workspace_size(int32_t op, int64_t m, int64_t n, int64_t k, int32_t group,

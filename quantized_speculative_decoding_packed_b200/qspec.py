@@ -28,9 +28,12 @@ EXPORTED = ("qspec_quantize_weights", "qspec_quant_act", "qspec_cast_bf16", "qsp
             "qspec_workspace_status",
             "qspec_status_string", "qspec_gemm_w4a16_noalloc", "qspec_gemm_w4a16_noalloc_status",
             "qspec_kv_append", "qspec_attn_decode", "qspec_attn_workspace_size", "qspec_kv_commit",
-            "qspec_abi_version")
+            "qspec_rope_table", "qspec_qkv_rope_append", "qspec_attn_prefill",
+            "qspec_attn_prefill_workspace_size", "qspec_attn_prefix",
+            "qspec_attn_prefix_workspace_size", "qspec_abi_version")
 ABI_VERSION = 5
 HEAD_DIM = 128           # the KV-cache calls' head dimension
+ROPE_INTERLEAVED, ROPE_Q_FP32 = 1, 2
 GEMM_WEIGHTS_READY = 1   # flag: wq/ws are not written by work still in flight
 GEMM_TEST_STALL = 0x100  # test hook: the GEMM's first wait runs out (QSPEC_GEMM_TEST_STALL)
 GEMM_FUSED_QUANT = 0x2   # drafting modes, m <= 32: activations quantized inside the GEMM kernel
@@ -48,8 +51,8 @@ def _load() -> ctypes.CDLL:
             f"libqspec.so not found at {_LIB_PATH}; build it with "
             "`python -m quantized_speculative_decoding_packed_b200.build`")
     lib = ctypes.CDLL(_LIB_PATH)
-    P, I64, I32, U32, SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32,
-                            ctypes.c_size_t)
+    P, I64, I32, U32, SZ, F32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32,
+                                 ctypes.c_size_t, ctypes.c_float)
     lib.qspec_quantize_weights.argtypes = [P, I64, I64, I32, P, P, P]
     lib.qspec_quant_act.argtypes = [P, I64, I64, P, P, P]
     lib.qspec_cast_bf16.argtypes = [P, I64, I64, I64, P, P]
@@ -73,6 +76,16 @@ def _load() -> ctypes.CDLL:
     lib.qspec_attn_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32]
     lib.qspec_attn_workspace_size.restype = SZ
     lib.qspec_kv_commit.argtypes = [P, P, I32, I32, P, SZ, P]
+    lib.qspec_rope_table.argtypes = [P, I32, I64, P, P]
+    lib.qspec_qkv_rope_append.argtypes = [P, I64, I64, I32, P, I32, I32, I32, P, P, F32, P, I64, I32, P, P,
+                                          I32, P, P, I32, P, I64, U32, P, SZ, P]
+    lib.qspec_attn_prefill.argtypes = [P, I64, I64, I32, P, I32, I32, I32, P, P, P, I32, P, I64, P, SZ, P]
+    lib.qspec_attn_prefix.argtypes = [P, I64, I64, I32, P, I32, I32, I32, P, I32, P, P, I32, P, P, I32, P,
+                                      P, I64, P, SZ, P]
+    lib.qspec_attn_prefill_workspace_size.argtypes = []
+    lib.qspec_attn_prefill_workspace_size.restype = SZ
+    lib.qspec_attn_prefix_workspace_size.argtypes = [I64, I32, I32]
+    lib.qspec_attn_prefix_workspace_size.restype = SZ
     lib.qspec_status_string.argtypes = [I32]
     lib.qspec_status_string.restype = ctypes.c_char_p
     for name in ("qspec_quantize_weights", "qspec_quant_act", "qspec_cast_bf16", "qspec_gemm_w4a4",
@@ -80,7 +93,8 @@ def _load() -> ctypes.CDLL:
                  "qspec_gemm_w4a16", "qspec_spec_accept", "qspec_spec_accept_greedy",
                  "qspec_workspace_status",
                  "qspec_gemm_w4a16_noalloc", "qspec_gemm_w4a16_noalloc_status",
-                 "qspec_kv_append", "qspec_attn_decode", "qspec_kv_commit"):
+                 "qspec_kv_append", "qspec_attn_decode", "qspec_kv_commit", "qspec_rope_table",
+                 "qspec_qkv_rope_append", "qspec_attn_prefill", "qspec_attn_prefix"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.qspec_abi_version() != ABI_VERSION:
         raise ImportError(f"{_LIB_PATH} has ABI version {lib.qspec_abi_version()}, "
@@ -427,3 +441,208 @@ def kv_commit(lens: torch.Tensor, n_accepted: torch.Tensor, l_max: int,
     _check(LIB.qspec_kv_commit(_ptr(lens), _ptr(n_accepted), lens.numel(), l_max, _ptr(work),
                                nbytes, _stream(stream)), "qspec_kv_commit")
     return lens
+
+
+# ---------------------------------------------------------------- the prompt path
+# Default workspaces of the prompt attention, by device and stream: calls on two
+# streams have two.  One that has become too small is kept, for a captured graph may
+# still write to it.
+_PROMPT_WS: dict = {}
+_PROMPT_WS_RETIRED: list = []
+
+
+def _new_prompt_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def prompt_workspace(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
+    """A scratch buffer of at least `nbytes` bytes for the prompt attention calls on one stream.
+
+    Under stream capture the buffer belongs to the graph alone.  Graphs that share a buffer
+    passed as `work` must not run at the same time.
+    """
+    if torch.cuda.is_current_stream_capturing():
+        return _new_prompt_workspace(nbytes, device)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    key = (device, s.cuda_stream)
+    cur = _PROMPT_WS.get(key)
+    if cur is None or cur.numel() < nbytes:
+        if cur is not None:
+            _PROMPT_WS_RETIRED.append(cur)
+            nbytes = max(nbytes, 2 * cur.numel())
+        with torch.cuda.stream(s):
+            cur = _new_prompt_workspace(nbytes, device)
+        _PROMPT_WS[key] = cur
+    return cur
+
+
+_PREFILL_WS_SIZE: dict = {}
+
+
+def attn_prefill_workspace_size() -> int:
+    """Bytes that attn_prefill needs on the current device (0 where it does not run)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if dev not in _PREFILL_WS_SIZE:
+        _PREFILL_WS_SIZE[dev] = int(LIB.qspec_attn_prefill_workspace_size())
+    return _PREFILL_WS_SIZE[dev]
+
+
+def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int) -> int:
+    return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q))
+
+
+def _tokens_check(t: torch.Tensor, dtype, name: str):
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor [tokens][columns] with unit column stride")
+
+
+def _packed_check(cu, lens: torch.Tensor, batch: int, n_tokens: int, columns: int, needed: int, name: str) -> None:
+    _need(lens, torch.int32, "lens")
+    if lens.numel() != batch:
+        raise ValueError(f"lens has {lens.numel()} entries for a cache of {batch} sequences")
+    if cu is not None:
+        _need(cu, torch.int32, "cu")
+        if cu.numel() != batch + 1:
+            raise ValueError(f"cu has {cu.numel()} entries, {batch + 1} are needed")
+    elif n_tokens == 0 or n_tokens % batch != 0:
+        raise ValueError(f"{name} has {n_tokens} rows, not a positive multiple of the batch {batch}")
+    if columns < needed:
+        raise ValueError(f"{name} has {columns} columns, {needed} are needed")
+
+
+def _prefix_len_check(prefix_len) -> None:
+    _need(prefix_len, torch.int32, "prefix_len")
+    if prefix_len.numel() != 1:
+        raise ValueError("prefix_len must have one element")
+
+
+def _same_device(*tensors) -> None:
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device: {t.device} and {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def rope_table(inv_freq: torch.Tensor, positions: int, table: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Angles of `positions` positions for qkv_rope_append: inv_freq fp64 [rot/2] -> fp32 [positions][rot],
+    cosines, then sines (computed in 64 bits)."""
+    _need(inv_freq, torch.float64, "inv_freq")
+    rot = 2 * inv_freq.numel()
+    if table is None:
+        table = torch.empty((positions, rot), dtype=torch.float32, device=inv_freq.device)
+    _need(table, torch.float32, "table")
+    if tuple(table.shape) != (positions, rot):
+        raise ValueError(f"table must be [{positions}][{rot}]")
+    _same_device(inv_freq, table)
+    _check(LIB.qspec_rope_table(_ptr(inv_freq), rot, positions, _ptr(table), _stream(stream)), "qspec_rope_table")
+    return table
+
+
+def qkv_rope_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    h_q: int, table: torch.Tensor | None, cu: torch.Tensor | None = None,
+                    prefix_len: torch.Tensor | None = None, q_gamma: torch.Tensor | None = None,
+                    k_gamma: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                    q_out: torch.Tensor | None = None, work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Norms and rotation of the queries and keys of packed tokens; keys and values into the caches.
+
+    qkv fp32 [tokens][(h_q + 2 h_kv) * 128]; the queries are returned in q_out: bf16 (the default, for
+    attn_prefill and attn_prefix) or fp32, which may be qkv[:, :h_q * 128] itself (for attn_decode on qkv).
+    table: rope_table's, or None for no rotation.  cu: int32 [batch + 1] starts of the sequences' tokens
+    (None: the same number for each).
+    """
+    _qkv_check(qkv)
+    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
+    n, cols = qkv.shape
+    _packed_check(cu, lens, b, n, cols, (h_q + 2 * h_kv) * HEAD_DIM, "qkv")
+    rot = positions = 0
+    if table is not None:
+        _need(table, torch.float32, "table")
+        positions, rot = table.shape
+    for gamma, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        if gamma is not None:
+            _need(gamma, torch.float32, name)
+            if gamma.numel() != HEAD_DIM:
+                raise ValueError(f"{name} must have {HEAD_DIM} entries")
+    if prefix_len is not None:
+        _prefix_len_check(prefix_len)
+    if q_out is None:
+        q_out = torch.empty((n, h_q * HEAD_DIM), dtype=torch.bfloat16, device=qkv.device)
+    if q_out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("q_out must be bf16 or fp32")
+    _tokens_check(q_out, q_out.dtype, "q_out")
+    if q_out.shape[0] != n or q_out.shape[1] < h_q * HEAD_DIM:
+        raise ValueError(f"q_out must be [{n}][{h_q * HEAD_DIM}]")
+    _same_device(qkv, lens, k_cache, v_cache, table, cu, prefix_len, q_gamma, k_gamma, q_out, work)
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_Q_FP32 if q_out.dtype == torch.float32 else 0)
+    _check(LIB.qspec_qkv_rope_append(
+        _ptr(qkv), qkv.stride(0), n, b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(q_gamma), _ptr(k_gamma), eps,
+        _ptr(table), positions, rot, _ptr(prefix_len), _ptr(lens), offset, _ptr(k_cache), _ptr(v_cache), l_max,
+        _ptr(q_out), q_out.stride(0), flags, _ptr(work), 0 if work is None else work.numel(), _stream(stream)),
+        "qspec_qkv_rope_append")
+    return q_out
+
+
+def _prompt_out(q: torch.Tensor, h_q: int, out):
+    if out is None:
+        return torch.empty((q.shape[0], h_q * HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+    _tokens_check(out, torch.bfloat16, "out")
+    if out.shape[0] != q.shape[0] or out.shape[1] < h_q * HEAD_DIM:
+        raise ValueError(f"out must be [{q.shape[0]}][{h_q * HEAD_DIM}]")
+    return out
+
+
+def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 h_q: int, out: torch.Tensor | None = None, work: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts over the cache: bf16 [tokens][h_q * 128] -> bf16 of the same shape.
+
+    Token i of sequence b (rows cu[b] .. cu[b + 1] - 1 of q) sees positions 0 .. lens[b] + i.  Rows behind the
+    last sequence are not written.
+    """
+    _tokens_check(q, torch.bfloat16, "q")
+    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
+    if cu is None:
+        raise ValueError("cu is needed")
+    _packed_check(cu, lens, b, q.shape[0], q.shape[1], h_q * HEAD_DIM, "q")
+    out = _prompt_out(q, h_q, out)
+    _same_device(q, cu, lens, k_cache, v_cache, out, work)
+    if work is None:
+        work = prompt_workspace(attn_prefill_workspace_size(), q.device, stream)
+    _check(LIB.qspec_attn_prefill(_ptr(q), q.stride(0), q.shape[0], b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(lens),
+                                  _ptr(k_cache), _ptr(v_cache), l_max, _ptr(out), out.stride(0), _ptr(work),
+                                  work.numel(), _stream(stream)), "qspec_attn_prefill")
+    return out
+
+
+def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                h_q: int, prefix_k: torch.Tensor, prefix_v: torch.Tensor, prefix_len: torch.Tensor,
+                cu: torch.Tensor | None = None, out: torch.Tensor | None = None, work: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Attention of a batch behind one shared prefix: bf16 [tokens][h_q * 128] -> bf16 of the same shape.
+
+    Token t of sequence b sees prefix_len positions of prefix_k, prefix_v (bf16 [h_kv][prefix_max][128]) and
+    positions 0 .. lens[b] + offset + t of its own cache.  cu None: the same number of tokens for each sequence
+    (drafting and verifying passes); else packed prompts.
+    """
+    _tokens_check(q, torch.bfloat16, "q")
+    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
+    _packed_check(cu, lens, b, q.shape[0], q.shape[1], h_q * HEAD_DIM, "q")
+    _need(prefix_k, torch.bfloat16, "prefix_k")
+    _need(prefix_v, torch.bfloat16, "prefix_v")
+    if prefix_k.dim() != 3 or prefix_k.shape != prefix_v.shape or prefix_k.shape[0] != h_kv or prefix_k.shape[2] != HEAD_DIM:
+        raise ValueError(f"prefix_k and prefix_v must both be [{h_kv}][positions][{HEAD_DIM}]")
+    _prefix_len_check(prefix_len)
+    out = _prompt_out(q, h_q, out)
+    _same_device(q, cu, lens, k_cache, v_cache, prefix_k, prefix_v, prefix_len, out, work)
+    if work is None:
+        work = prompt_workspace(attn_prefix_workspace_size(q.shape[0], b, h_q), q.device, stream)
+    _check(LIB.qspec_attn_prefix(_ptr(q), q.stride(0), q.shape[0], b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(lens),
+                                 offset, _ptr(k_cache), _ptr(v_cache), l_max, _ptr(prefix_k), _ptr(prefix_v),
+                                 prefix_k.shape[1], _ptr(prefix_len), _ptr(out), out.stride(0), _ptr(work),
+                                 work.numel(), _stream(stream)), "qspec_attn_prefix")
+    return out
