@@ -12,11 +12,13 @@
 // relative rounding.
 //
 // A CTA per SM works through its share of the items (prompt_schedule.cuh).
+//   warp 10: finds the share's items and passes them on (ring of 4);
 //   warp 8: TMA of queries (ring of two tiles) and of key and value tiles
 //           (ring of 5 x 32 KB);
 //   warp 9: tcgen05.mma: S of the next step before P V of the current one;
 //   warps 0-3, 4-7: the softmax of slots 0 and 1, a thread for each row.  A slot
-//           is a tile of S, and of O, in tensor memory; P takes S's place.
+//           is a tile of S, and of O, in tensor memory; P takes S's place;
+//   warp 11: clears the rows of sequences that are refused.
 // With two row tiles, each has a slot, and both use every key tile.  With one,
 // the slots take alternate key tiles and are joined at the end of the item.
 // A piece of a split item is left in the workspace as (m, l, O); a second
@@ -25,6 +27,7 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "device_common.cuh"
@@ -34,10 +37,15 @@
 namespace qspec {
 
 constexpr int kPaStages = 5;
+constexpr int kPaItems = 4;                                  // items passed on ahead
 constexpr int kPaThreads = 384;
 constexpr int kPaTileBytes = 128 * kHeadDim * 2;             // 32 KB: a tile of Q, K or V
 constexpr float kScoreLog2 = kInvSqrtHeadDim * 1.4426950408889634f;   // scores in powers of two
 constexpr float kRaise = 8.f;
+
+// How a shared prefix is taken.
+enum : int { kPaNoPrefix = 0, kPaPrefixOnce = 1, kPaPrefixAhead = 2 };
+constexpr int kPaAheadRows = 96;
 
 struct PromptArgs {
   const int32_t* cu;           // null: t_new tokens for every sequence
@@ -47,12 +55,12 @@ struct PromptArgs {
   uint8_t* work;
   int64_t ld_out;
   int64_t off_start, off_desc, off_ml, off_o, off_row_ml, off_row_o;
-  int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max;
+  int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
 };
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
 struct PaJoin {
-  int32_t valid, first, tok0, n_tok, g, pad[3];
+  int32_t valid, first, tok, tokens, g, pad[3];
 };
 
 struct PaMeta {
@@ -61,8 +69,9 @@ struct PaMeta {
   int32_t prefix;              // the prefix's length, -1 where it is refused
 };
 
-// Workspace: status word, what the GEMMs keep there, then per CTA two pieces of two row tiles;
-// with a prefix, for each (token, head) a row for its prefix and one for its own keys.
+// Workspace: status word, what the GEMMs keep there, then per CTA two pieces of two row tiles
+// (O in blocks of 4 columns: [32][128 rows][4]); with a prefix taken once, for each (token, head)
+// a row for its prefix and one for its own keys.
 constexpr int64_t kPaOffMeta = 8192;
 struct PaLayout {
   int64_t off_start, off_desc, off_ml, off_o, off_row_ml, off_row_o, total;
@@ -160,259 +169,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// ---------------------------------------------------------------- walking the items
-// Sequence b's packed tokens and the keys before them; n = 0 where its
-// offsets or its length are not those of the cache.
-struct PaSequence {
-  int tok0, n;
-  int64_t base;
-  bool bad;
-};
-__device__ __forceinline__ PaSequence pa_sequence(const PromptArgs& a, int b) {
-  PaSequence s;
-  int n;
-  s.bad = false;
-  if (a.cu) {
-    s.tok0 = a.cu[b];
-    const int64_t end = a.cu[b + 1];
-    s.bad = s.tok0 < 0 || end < s.tok0 || end > a.n_tok;
-    n = s.bad ? 0 : static_cast<int>(end - s.tok0);
-  } else {
-    s.tok0 = b * a.t_new;
-    n = a.t_new;
-  }
-  const int64_t len = a.lens[b];
-  s.base = len + a.offset;
-  s.bad = s.bad || len < 0 || s.base + n > a.l_max;
-  s.n = s.bad ? 0 : n;
-  return s;
-}
-
-// The tokens that take part in the prefix's items.
-__device__ __forceinline__ int pa_packed_tokens(const PromptArgs& a) {
-  if (!a.cu) return a.n_tok;
-  const int end = a.cu[a.batch];
-  return end < 0 ? 0 : (end > a.n_tok ? a.n_tok : end);
-}
-
-struct PaShare {
-  int64_t s0, s1, total;
-  int64_t start;               // of the first item
-  int b, g, i;                 // the first item; b < 0: the prefix's
-  int ctas, prefix;
-};
-
-struct PaWalk {
-  int64_t start;
-  Run run;
-  int b, g, i, items, tok0;
-  // the item at hand
-  int w, n, j0, j1, tokens;
-
-  __device__ __forceinline__ void load_run(const PromptArgs& a, int prefix) {
-    run.tpt = a.tpt;
-    if (b < 0) {
-      run.n = pa_packed_tokens(a);
-      run.base = -1;
-      run.keys = prefix;
-      tok0 = 0;
-    } else {
-      const PaSequence s = pa_sequence(a, b);
-      run.n = s.n;
-      run.base = s.base;
-      run.keys = 0;
-      tok0 = s.tok0;
-    }
-    items = run_items(run);
-  }
-  __device__ __forceinline__ void item(const PaShare& sh) {
-    tokens = item_tokens(run, i);
-    w = tokens > run.tpt ? 2 : 1;
-    n = static_cast<int>((item_keys(run, i, tokens) + 127) / 128);
-    share_tiles(start, w, n, sh.s0, sh.s1, &j0, &j1);
-  }
-  __device__ __forceinline__ void begin(const PromptArgs& a, const PaShare& sh) {
-    b = sh.b; g = sh.g; i = sh.i; start = sh.start;
-    load_run(a, sh.prefix);
-  }
-  // Moves to the next item with key tiles in the share; false where there is none.
-  __device__ __forceinline__ bool find(const PromptArgs& a, const PaShare& sh, bool first) {
-    for (;;) {
-      if (!first) {
-        start += static_cast<int64_t>(w) * n + kItemCost;
-        if (++i >= items) {
-          i = 0;
-          if (++g >= a.h_kv) {
-            g = 0;
-            do {
-              if (++b >= a.batch) return false;
-              load_run(a, sh.prefix);
-            } while (run.n == 0);
-          }
-        }
-      }
-      first = false;
-      if (start >= sh.s1) return false;
-      item(sh);
-      if (j0 < j1) return true;
-    }
-  }
-  // Key tiles of the first row tile in this share end here (the second sees more).
-  __device__ __forceinline__ int end_of_first() const {
-    if (w == 1 || run.base < 0) return j1;
-    const int n0 = static_cast<int>((item_keys(run, i, run.tpt) + 127) / 128);
-    return n0 < j1 ? (n0 > j0 ? n0 : j0) : j1;
-  }
-  __device__ __forceinline__ int64_t last_keys() const { return item_keys(run, i, tokens); }
-};
-
-// Barriers and small exchanges in shared memory.
-struct PaShared {
-  uint64_t kv_full[kPaStages], kv_empty[kPaStages], q_full[2], q_empty[2];
-  uint64_t s_ready[2], p_ready[2], pv_done[2], o_free, ml_ready, drained;
-  PaShare share;
-  int64_t warp_sums[kPaThreads / 32];
-  int64_t found_start, found_cost;
-  int found_b;
-  int abort_flag;
-  uint32_t tmem;
-  float2 ml[2][128];
-};
-constexpr int kPaTilesBytes = (2 + kPaStages) * kPaTileBytes;          // Q, K and V tiles, then PaShared
-constexpr int kPaSmemBytes = kPaTilesBytes + static_cast<int>(sizeof(PaShared));
-static_assert(kPaSmemBytes <= 227 * 1024, "shared memory of a CTA");
-
-// The costs of all sequences, their sum, and this CTA's first item.
-__device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int prefix = 0;
-  if (a.prefix_len) {
-    prefix = *a.prefix_len;
-    if (prefix < 0 || prefix > a.prefix_max) prefix = 0;
-  }
-  Run pr;
-  pr.n = prefix > 0 ? pa_packed_tokens(a) : 0;
-  pr.tpt = a.tpt;
-  pr.base = -1;
-  pr.keys = prefix;
-  const int64_t prefix_head = run_cost(pr);
-  const int64_t prefix_all = prefix_head * a.h_kv;
-
-  int64_t before = prefix_all;         // the cost before the chunk of sequences at hand
-  int64_t cost = 0, at = 0;
-  auto scan = [&](int b) {             // block-wide: this thread's cost and the costs before it
-    cost = 0;
-    if (b < a.batch) {
-      const PaSequence s = pa_sequence(a, b);
-      Run r;
-      r.n = s.n;
-      r.tpt = a.tpt;
-      r.base = s.base;
-      r.keys = 0;
-      cost = run_cost(r) * a.h_kv;
-    }
-    int64_t incl = cost;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (lane == 31) sm.warp_sums[warp] = incl;
-    __syncthreads();
-    int64_t all = 0;
-    at = before + incl - cost;
-#pragma unroll
-    for (int k = 0; k < kPaThreads / 32; ++k) {
-      const int64_t s = sm.warp_sums[k];
-      if (k < warp) at += s;
-      all += s;
-    }
-    before += all;
-    __syncthreads();
-  };
-  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) scan(b0 + tid);
-  const int64_t total = before;
-  const int ctas = working_ctas(total, gridDim.x);
-  const int c = blockIdx.x;
-  const int64_t s0 = c < ctas ? share_start(total, ctas, c) : total;
-  const int64_t s1 = c < ctas ? share_start(total, ctas, c + 1) : total;
-  if (tid == 0) {
-    sm.share.s0 = s0;
-    sm.share.s1 = s1;
-    sm.share.total = total;
-    sm.share.ctas = ctas;
-    sm.share.prefix = prefix;
-    sm.found_b = -1;
-  }
-  if (c == 0 && tid == 0) {
-    PaMeta* meta = reinterpret_cast<PaMeta*>(a.work + kPaOffMeta);
-    meta->total = total;
-    meta->ctas = ctas;
-    meta->prefix = a.prefix_len && *a.prefix_len != prefix ? -1 : prefix;
-  }
-  __syncthreads();
-  int64_t* const starts = a.prefix_len ? reinterpret_cast<int64_t*>(a.work + a.off_start) : nullptr;
-  before = prefix_all;
-  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
-    const int b = b0 + tid;
-    if (a.batch > kPaThreads) scan(b);           // else this thread's values still stand
-    if (b < a.batch) {
-      if (c == 0 && starts) starts[b] = at;
-      if (cost > 0 && at <= s0 && s0 < at + cost) {
-        sm.found_b = b;
-        sm.found_start = at;
-        sm.found_cost = cost / a.h_kv;
-      }
-    }
-  }
-  __syncthreads();
-  if (s0 < s1 && warp == 0) {
-    int b = sm.found_b, g;
-    int64_t start, head_cost;
-    Run r;
-    if (s0 < prefix_all) {
-      b = -1;
-      start = 0;
-      head_cost = prefix_head;
-      r = pr;
-    } else {
-      start = sm.found_start;
-      head_cost = sm.found_cost;
-      const PaSequence s = pa_sequence(a, b);
-      r.n = s.n;
-      r.tpt = a.tpt;
-      r.base = s.base;
-      r.keys = 0;
-    }
-    g = static_cast<int>((s0 - start) / head_cost);
-    start += g * head_cost;
-    // the last item that starts at or before s0: [lo, lo + n) narrowed 32-fold
-    int lo = 0, n = run_items(r);
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const bool le = lane * step < n && (lane == 0 || start + cost_before(r, lo + lane * step) <= s0);
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
-    if (lane == 0) {
-      sm.share.b = b;
-      sm.share.g = g;
-      sm.share.i = lo;
-      sm.share.start = start + cost_before(r, lo);
-    }
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------- the softmax of one tile
-// Row of S in tensor memory -> P (bf16) in its place; m, l updated.  Returns
-// the factor by which what is in O has to be scaled (1: nothing to do).
-struct PaRow {
-  float m;                     // the maximum in use (-inf: none yet)
-  float l;
-};
-
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -436,114 +192,430 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return d;
 }
 
-// ---------------------------------------------------------------- the roles of the warps
-__device__ __forceinline__ void pa_load(const PromptArgs& a, PaShared& sm, uint32_t q_s, uint32_t kv_s,
-                                        const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                        const CUtensorMap* tm_pk, const CUtensorMap* tm_pv) {
-  const int lane = threadIdx.x & 31;
-  const PaShare& sh = sm.share;
-  uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
-  volatile int* const abort_flag = &sm.abort_flag;
-  if (lane == 0) {
-    uint32_t ring = 0, qn = 0;
-    bool ok = true;
-    PaWalk it;
-    it.begin(a, sh);
-    for (bool first = true; ok && it.find(a, sh, first); first = false) {
-      const CUtensorMap* mk = it.b < 0 ? tm_pk : tm_k;
-      const CUtensorMap* mv = it.b < 0 ? tm_pv : tm_v;
-      const int head = it.b < 0 ? it.g : it.b * a.h_kv + it.g;
-      // (a first row tile that sees none of the share's keys is left out)
-      for (int x = it.w == 2 && it.end_of_first() == it.j0; x < it.w && ok; ++x, ++qn) {
-        const uint32_t slot = qn & 1;
-        ok = mbar_wait(smem_u32(&sm.q_empty[slot]), ((qn >> 1) & 1) ^ 1, abort_flag, status);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&sm.q_full[slot]);
-        const uint32_t dst = q_s + slot * kPaTileBytes;
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.tpt * a.group) * kHeadDim * 2);
-        const int tok = it.tok0 + (it.i * 2 + x) * a.tpt;
-        tma_load_3d(dst, tm_q, bar, 0, it.g * a.group, tok);
-        tma_load_3d(dst + kPaTileBytes / 2, tm_q, bar, 64, it.g * a.group, tok);
-      }
-      for (int j = it.j0; j < it.j1 && ok; ++j) {
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
+// Of each 8 pairs of weights so many come from exp2_poly: the special function
+// unit, at 4 a cycle for each quarter of an SM, is what the softmax waits for.
+constexpr int kPolyPairs = 3;
+
+// 2^x for x <= 2^7 without the special function unit: x = k + r with k the nearest
+// integer (by adding 1.5 x 2^23, whose last bits then hold k), 2^r by a
+// polynomial, k added to its exponent.  The polynomial is the one of degree 4
+// with the least relative error on |r| <= 1/2 (2.6e-6, from a weighted
+// least-squares fit), far below the 2^-9 of the bf16 that its result becomes.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 big = make_float2(12582912.f, 12582912.f), neg = make_float2(-12582912.f, -12582912.f);
+  const float2 t = add2(x, big);
+  const float2 k = add2(t, neg);
+  const float2 r = fma2(k, make_float2(-1.f, -1.f), x);
+  float2 y = fma2(r, make_float2(0x1.3997d6p-7f, 0x1.3997d6p-7f), make_float2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
+  y = fma2(y, r, make_float2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
+  y = fma2(y, r, make_float2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
+  y = fma2(y, r, make_float2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+  y.x = __int_as_float((__float_as_int(t.x) << 23) + __float_as_int(y.x));
+  y.y = __int_as_float((__float_as_int(t.y) << 23) + __float_as_int(y.y));
+  return y;
+}
+
+// ---------------------------------------------------------------- finding the items
+// Sequence b's packed tokens and the keys before them; n = 0 where its
+// offsets or its length are not those of the cache.
+struct PaSequence {
+  int tok0, n, base;
+  bool bad;
+};
+__device__ __forceinline__ PaSequence pa_sequence(const PromptArgs& a, int b) {
+  PaSequence s;
+  int n;
+  s.bad = false;
+  const int64_t len = a.lens[b];
+  if (a.cu) {
+    s.tok0 = a.cu[b];
+    const int end = a.cu[b + 1];
+    s.bad = s.tok0 < 0 || end < s.tok0 || end > a.n_tok;
+    n = s.bad ? 0 : end - s.tok0;
+  } else {
+    s.tok0 = b * a.t_new;
+    n = a.t_new;
+  }
+  const int64_t base = len + a.offset;
+  s.bad = s.bad || len < 0 || base + n > a.l_max;
+  s.n = s.bad ? 0 : n;
+  s.base = s.bad ? 0 : static_cast<int>(base);
+  return s;
+}
+
+// The tokens that take part in the items of a prefix taken once.
+__device__ __forceinline__ int pa_packed_tokens(const PromptArgs& a) {
+  if (!a.cu) return a.n_tok;
+  const int end = a.cu[a.batch];
+  return end < 0 ? 0 : (end > a.n_tok ? a.n_tok : end);
+}
+
+// The prefix's length; -1 where it is refused.
+__device__ __forceinline__ int pa_prefix(const PromptArgs& a) {
+  if (!a.prefix_len) return 0;
+  const int p = *a.prefix_len;
+  return p < 0 || p > a.prefix_max ? -1 : p;
+}
+
+__device__ __forceinline__ Run pa_prefix_run(const PromptArgs& a, int prefix) {
+  Run r;
+  r.n = prefix > 0 && a.mode == kPaPrefixOnce ? pa_packed_tokens(a) : 0;
+  r.tpt = a.tpt;
+  r.base = -1;
+  r.pre = (prefix + 127) >> 7;
+  return r;
+}
+__device__ __forceinline__ Run pa_own_run(const PromptArgs& a, const PaSequence& s, int prefix) {
+  Run r;
+  r.n = prefix < 0 ? 0 : s.n;
+  r.tpt = a.tpt;
+  r.base = s.base;
+  r.pre = a.mode == kPaPrefixAhead ? (prefix + 127) >> 7 : 0;
+  return r;
+}
+
+// An item, or what of it lies in this CTA's share, as the warps get it.
+struct PaItem {
+  int32_t tok, tokens;         // packed tokens; tokens = 0: no more items
+  int32_t g, head;             // KV head; its place among the caches' heads
+  int32_t j0, j1, end0;        // key tiles of the share; those that the first of two row tiles sees end at end0
+  int32_t pre_tiles, pre;      // the first key tiles are the prefix's, with so many keys
+  int32_t sees;                // own keys that the first token sees (each later one sees one more)
+  int32_t flags, first_cta;
+};
+enum : int { kPaTwo = 1, kPaWhole = 2, kPaCarried = 4, kPaEnds = 8, kPaOnce = 16 };
+
+struct PaShare {
+  int64_t s0, s1, total;
+  int64_t start;               // of the first item
+  int b, g, i;                 // the first item; b < 0: the prefix's
+  int ctas, prefix;
+};
+
+// Barriers and small exchanges in shared memory.
+struct PaShared {
+  uint64_t kv_full[kPaStages], kv_empty[kPaStages], q_full[2], q_empty[2];
+  uint64_t s_ready[2], p_ready[2], pv_done[2], o_free, ml_ready, drained;
+  uint64_t item_full[kPaItems], item_empty[kPaItems];
+  PaItem items[kPaItems];
+  PaShare share;
+  int64_t warp_sums[kPaThreads / 32];
+  int64_t found_start, found_cost;
+  int found_b;
+  int abort_flag;
+  uint32_t tmem;
+  float2 ml[2][128];
+};
+constexpr int kPaTilesBytes = (2 + kPaStages) * kPaTileBytes;          // Q, K and V tiles, then PaShared
+constexpr int kPaSmemBytes = kPaTilesBytes + static_cast<int>(sizeof(PaShared));
+static_assert(kPaSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+// The costs of all sequences, their sum, and this CTA's first item.
+__device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int prefix = pa_prefix(a);
+  const Run pr = pa_prefix_run(a, prefix);
+  const int64_t prefix_head = run_cost(pr);
+  const int64_t prefix_all = prefix_head * a.h_kv;
+
+  int64_t before = prefix_all;         // the cost before the chunk of sequences at hand
+  int64_t cost = 0, at = 0;            // of one KV head of this thread's sequence; before the sequence
+  auto scan = [&](int b) {
+    cost = b < a.batch ? run_cost(pa_own_run(a, pa_sequence(a, b), prefix)) : 0;
+    const int64_t mine = cost * a.h_kv;
+    int64_t incl = mine;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t st = ring % kPaStages;
-          ok = ok && mbar_wait(smem_u32(&sm.kv_empty[st]), ((ring / kPaStages) & 1) ^ 1, abort_flag, status);
-          if (!ok) break;
-          const uint32_t bar = smem_u32(&sm.kv_full[st]);
-          mbar_arrive_expect_tx(bar, kPaTileBytes);
-          tma_load_4d(kv_s + st * kPaTileBytes, kv ? mv : mk, bar, 0, j * 128, 0, head);
-          ++ring;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (lane == 31) sm.warp_sums[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+    at = before + incl - mine;
+#pragma unroll
+    for (int k = 0; k < kPaThreads / 32; ++k) {
+      const int64_t s = sm.warp_sums[k];
+      if (k < warp) at += s;
+      all += s;
+    }
+    before += all;
+    if (a.batch > kPaThreads) __syncthreads();   // the sums are written again
+  };
+  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) scan(b0 + tid);
+  const int64_t total = before;
+  const int ctas = working_ctas(total, gridDim.x);
+  const int c = blockIdx.x;
+  const int64_t s0 = c < ctas ? share_start(total, ctas, c) : total;
+  const int64_t s1 = c < ctas ? share_start(total, ctas, c + 1) : total;
+  if (tid == 0) {
+    sm.share.s0 = s0;
+    sm.share.s1 = s1;
+    sm.share.total = total;
+    sm.share.ctas = ctas;
+    sm.share.prefix = prefix;
+    if (c == 0) {
+      PaMeta* meta = reinterpret_cast<PaMeta*>(a.work + kPaOffMeta);
+      meta->total = total;
+      meta->ctas = ctas;
+      meta->prefix = prefix;
+    }
+  }
+  int64_t* const starts = a.mode == kPaPrefixOnce ? reinterpret_cast<int64_t*>(a.work + a.off_start) : nullptr;
+  before = prefix_all;
+  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
+    const int b = b0 + tid;
+    if (a.batch > kPaThreads) scan(b);           // else this thread's values still stand
+    if (b < a.batch) {
+      if (c == 0 && starts) starts[b] = at;
+      if (cost > 0 && at <= s0 && s0 < at + cost * a.h_kv) {
+        sm.found_b = b;
+        sm.found_start = at;
+        sm.found_cost = cost;
+      }
+    }
+  }
+  __syncthreads();
+  if (s0 < s1 && warp == 10) {
+    int b = -1;
+    int64_t start = 0, head_cost = prefix_head;
+    Run r = pr;
+    if (s0 >= prefix_all) {
+      b = sm.found_b;
+      start = sm.found_start;
+      head_cost = sm.found_cost;
+      r = pa_own_run(a, pa_sequence(a, b), prefix);
+    }
+    const int g = static_cast<int>(div_u64(s0 - start, head_cost));
+    start += g * head_cost;
+    // the last item that starts at or before s0: [lo, lo + n) narrowed 32-fold
+    int lo = 0, n = run_items(r);
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const bool le = lane * step < n && (lane == 0 || start + cost_before(r, lo + lane * step) <= s0);
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
+      lo += k * step;
+      n = min(step, n - k * step);
+    }
+    if (lane == 0) {
+      sm.share.b = b;
+      sm.share.g = g;
+      sm.share.i = lo;
+      sm.share.start = start + cost_before(r, lo);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the roles of the warps
+// Warp 10: the share's items in order, into the ring.
+__device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  const PaShare sh = sm.share;
+  uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  uint32_t count = 0;
+  auto pass = [&](const PaItem& it) -> bool {
+    const uint32_t slot = count % kPaItems;
+    if (!warp_wait(smem_u32(&sm.item_empty[slot]), ((count / kPaItems) & 1) ^ 1, &sm.abort_flag, status)) return false;
+    if (lane == 0) {
+      sm.items[slot] = it;
+      mbar_arrive(smem_u32(&sm.item_full[slot]));
+    }
+    __syncwarp();
+    ++count;
+    return true;
+  };
+  PaItem it;
+  if (sh.s0 < sh.s1) {
+    int b = sh.b, g = sh.g, i = sh.i, block = -1;
+    int64_t start = sh.start;
+    PaSequence mine;             // of sequence block * 32 + lane
+    mine.n = mine.tok0 = mine.base = 0;
+    Run run = pa_prefix_run(a, sh.prefix);
+    int tok0 = 0;
+    auto load = [&]() {          // sequence b's run
+      if ((b >> 5) != block) {
+        block = b >> 5;
+        if (block * 32 + lane < a.batch) mine = pa_sequence(a, block * 32 + lane);
+        else mine.n = 0;
+      }
+      PaSequence s;
+      s.n = __shfl_sync(0xffffffffu, mine.n, b & 31);
+      s.tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
+      s.base = __shfl_sync(0xffffffffu, mine.base, b & 31);
+      run = pa_own_run(a, s, sh.prefix);
+      tok0 = s.tok0;
+    };
+    if (b >= 0) load();
+    int items = run_items(run);
+    while (start < sh.s1) {
+      const int tokens = item_tokens(run, i);
+      const int w = tokens > run.tpt ? 2 : 1;
+      const int n = item_tiles(run, i, tokens);
+      share_tiles(start, w, n, sh.s0, sh.s1, &it.j0, &it.j1);
+      if (it.j0 < it.j1) {
+        const int first = i * 2 * run.tpt;
+        it.tok = tok0 + first;
+        it.tokens = tokens;
+        it.g = g;
+        it.head = b < 0 ? g : b * a.h_kv + g;
+        it.end0 = w == 1 ? it.j1 : min(it.j1, max(it.j0, item_tiles(run, i, run.tpt)));
+        it.pre_tiles = run.pre;
+        it.pre = sh.prefix;
+        it.sees = run.base + first + 1;
+        const bool whole = it.j0 == 0 && it.j1 == n;
+        it.flags = (w == 2 ? kPaTwo : 0) | (whole ? kPaWhole : 0) | (start < sh.s0 ? kPaCarried : 0) |
+                   (it.j1 == n ? kPaEnds : 0) | (b < 0 ? kPaOnce : 0);
+        it.first_cta = whole ? blockIdx.x : share_owner(sh.total, sh.ctas, start);
+        if (!pass(it)) return;
+      }
+      start += cost_of(w, n);
+      if (++i >= items) {
+        i = 0;
+        if (++g >= a.h_kv) {
+          g = 0;
+          do {
+            if (++b >= a.batch) break;
+            load();
+          } while (run.n == 0);
+          if (b >= a.batch) break;
+          items = run_items(run);
         }
       }
     }
-    if (!ok) {
-      // given up: let the copies in flight land before shared memory goes
-      const uint32_t kv_from = ring > kPaStages ? ring - kPaStages : 0;
-      for (uint32_t r = kv_from; r < ring; ++r)
-        mbar_wait_drain(smem_u32(&sm.kv_full[r % kPaStages]), (r / kPaStages) & 1);
-      for (uint32_t r = qn > 2 ? qn - 2 : 0; r < qn; ++r)
-        mbar_wait_drain(smem_u32(&sm.q_full[r & 1]), (r >> 1) & 1);
-    }
   }
-  __syncwarp();
+  it.tokens = 0;
+  pass(it);
 }
 
-__device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, uint32_t tmem, uint32_t q_s, uint32_t kv_s) {
-  const int lane = threadIdx.x & 31;
-  const PaShare& sh = sm.share;
+// Waits for item `count` of the ring; its readers say when they have it.
+template <bool kCall>
+__device__ __forceinline__ bool pa_item_wait(PaShared& sm, uint32_t count, uint32_t* status) {
+  const uint32_t bar = smem_u32(&sm.item_full[count % kPaItems]);
+  if constexpr (kCall) return warp_wait(bar, (count / kPaItems) & 1, &sm.abort_flag, status);
+  else return pa_wait(bar, (count / kPaItems) & 1, &sm.abort_flag, status);
+}
+
+// Warp 8: loads.
+__device__ __forceinline__ void pa_load(const PromptArgs& a, PaShared& sm, uint32_t q_s, uint32_t kv_s,
+                                        const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                        const CUtensorMap* tm_pk, const CUtensorMap* tm_pv) {
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   volatile int* const abort_flag = &sm.abort_flag;
-  // The steps of the share in order: (row tile or alternate slot, key tile).
-  // S of the next step is issued before P V of the current one where its
-  // operands are there and its slot is another.
+  const uint32_t leader = elect_one_lane();
+  uint32_t ring = 0, qn = 0;
+  bool ok = true;
+  for (uint32_t count = 0;; ++count) {
+    ok = pa_item_wait<true>(sm, count, status);
+    if (!ok) break;
+    const PaItem it = sm.items[count % kPaItems];
+    __syncwarp();
+    if (leader) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+    if (it.tokens == 0) break;
+    const bool two = it.flags & kPaTwo;
+    // (a first row tile that sees none of the share's keys is left out)
+    for (int x = two && it.end0 == it.j0 ? 1 : 0; x < (two ? 2 : 1) && ok; ++x) {
+      const uint32_t slot = qn & 1;
+      ok = warp_wait(smem_u32(&sm.q_empty[slot]), ((qn >> 1) & 1) ^ 1, abort_flag, status);
+      if (!ok) break;
+      if (leader) {
+        const uint32_t bar = smem_u32(&sm.q_full[slot]);
+        const uint32_t dst = q_s + slot * kPaTileBytes;
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.tpt * a.group) * kHeadDim * 2);
+        tma_load_3d(dst, tm_q, bar, 0, it.g * a.group, it.tok + x * a.tpt);
+        tma_load_3d(dst + kPaTileBytes / 2, tm_q, bar, 64, it.g * a.group, it.tok + x * a.tpt);
+      }
+      ++qn;
+    }
+    for (int j = it.j0; j < it.j1 && ok; ++j) {
+      const bool pre = j < it.pre_tiles;
+      const int row = (pre ? j : j - it.pre_tiles) * 128;
+      const int head = pre ? it.g : it.head;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t st = ring % kPaStages;
+        ok = ok && warp_wait(smem_u32(&sm.kv_empty[st]), ((ring / kPaStages) & 1) ^ 1, abort_flag, status);
+        if (!ok) break;
+        if (leader) {
+          const uint32_t bar = smem_u32(&sm.kv_full[st]);
+          mbar_arrive_expect_tx(bar, kPaTileBytes);
+          tma_load_4d(kv_s + st * kPaTileBytes, kv ? (pre ? tm_pv : tm_v) : (pre ? tm_pk : tm_k), bar, 0, row, 0, head);
+        }
+        ++ring;
+      }
+    }
+    if (!ok) break;
+  }
+  if (!ok) {
+    // given up: let the copies in flight land before shared memory goes
+    for (uint32_t r = ring > kPaStages ? ring - kPaStages : 0; r < ring; ++r)
+      mbar_wait_drain(smem_u32(&sm.kv_full[r % kPaStages]), (r / kPaStages) & 1);
+    for (uint32_t r = qn > 2 ? qn - 2 : 0; r < qn; ++r)
+      mbar_wait_drain(smem_u32(&sm.q_full[r & 1]), (r >> 1) & 1);
+  }
+}
+
+// Warp 9: tensor cores.  The steps of the share in order: (row tile or alternate
+// slot, key tile).  S of the next step is issued before P V of the current one
+// where its operands are there and its slot is another.
+__device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, uint32_t tmem, uint32_t q_s, uint32_t kv_s) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  volatile int* const abort_flag = &sm.abort_flag;
   struct Step {
     uint32_t slot, k_ring, q_ring;     // the value tile is the next in the ring
     int pv_steps, tail;                // 16-key steps of P V; first unseen key of the tile (128: none)
     bool first, fresh;                 // first of its slot in the item, first of the item
     bool k_last, q_last;               // the last step on this key tile, on these queries
   };
-  PaWalk it;
-  it.begin(a, sh);
-  bool have = it.find(a, sh, true);
-  int j = 0, x = 0, end0 = 0;
-  int64_t last = 0;
-  uint32_t ring = 0, qn = 0, count = 0;      // key tiles x 2, query tiles, single-tile steps
-  uint32_t item_parity = 0;
-  bool entered = false;
+  PaItem it;
+  bool ok = true, entered = false;
+  int j = 0, x = 0;
+  uint32_t count = 0;                        // items taken
+  uint32_t ring = 0, qn = 0, singles = 0;    // key tiles x 2, query tiles, steps of items with one row tile
+  uint32_t parity = 0;
   auto next = [&](Step& s) -> bool {
-    if (!have) return false;
-    bool fresh = false;
+    const bool fresh = !entered;
     if (!entered) {
+      ok = pa_item_wait<true>(sm, count, status);
+      if (!ok) return false;
+      it = sm.items[count % kPaItems];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+      ++count;
+      if (it.tokens == 0) return false;
       entered = true;
-      fresh = true;
       j = it.j0;
-      end0 = it.end_of_first();
-      last = it.last_keys();
       x = 0;
-      item_parity = count & 1;
+      parity = singles & 1;
     }
-    const bool two = it.w == 2;
-    if (two && x == 0 && j >= end0) x = 1;
+    const bool two = it.flags & kPaTwo;
+    if (two && x == 0 && j >= it.end0) x = 1;
     s.fresh = fresh;
     if (two) {
       s.slot = x;
-      s.q_ring = qn + (x == 1 && end0 > it.j0);
+      s.q_ring = qn + (x == 1 && it.end0 > it.j0);
       s.first = j == it.j0;
       s.k_last = x == 1;
-      s.q_last = x == 0 ? j == end0 - 1 : j == it.j1 - 1;
+      s.q_last = x == 0 ? j == it.end0 - 1 : j == it.j1 - 1;
     } else {
-      s.slot = (item_parity + (j - it.j0)) & 1;
+      s.slot = (parity + (j - it.j0)) & 1;
       s.q_ring = qn;
       s.first = j - it.j0 < 2;
       s.k_last = true;
       s.q_last = j == it.j1 - 1;
     }
     s.k_ring = ring;
-    const int64_t left = last - static_cast<int64_t>(j) * 128;
-    s.tail = left >= 128 ? 128 : static_cast<int>(left);
-    s.pv_steps = (s.tail + 15) / 16;
+    const int left = j < it.pre_tiles ? it.pre - j * 128 : it.sees + it.tokens - 1 - (j - it.pre_tiles) * 128;
+    s.tail = min(left, 128);
+    s.pv_steps = (s.tail + 15) >> 4;
     // advance
     if (two && x == 0) {
       x = 1;
@@ -551,17 +623,15 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
       x = 0;
       ring += 2;
       if (++j >= it.j1) {
-        if (!two) count += it.j1 - it.j0;
-        qn += two && end0 > it.j0 ? 2 : 1;
+        if (!two) singles += it.j1 - it.j0;
+        qn += two && it.end0 > it.j0 ? 2 : 1;
         entered = false;
-        have = it.find(a, sh, false);
       }
     }
     return true;
   };
   uint32_t p_count = 0;                      // phases of p_ready: slot 0 in bit 0, slot 1 in bit 1
   uint32_t items_done = 0;
-  bool ok = true;
   const uint32_t leader = elect_one_lane();
   auto s_operands = [&](const Step& s, bool block) -> bool {
     const uint32_t kb = smem_u32(&sm.kv_full[s.k_ring % kPaStages]), kp = (s.k_ring / kPaStages) & 1;
@@ -626,6 +696,7 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
   }
   while (ok && more) {
     const bool has_next = next(nxt);
+    if (!ok) break;
     bool issued = false;
     if (has_next && nxt.slot != cur.slot && s_operands(nxt, false)) {
       issue_s(nxt);
@@ -647,9 +718,28 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
   }
 }
 
-__device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, uint32_t tmem, PaJoin* join) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const PaShare& sh = sm.share;
+// Among the four lanes of a quad, unit j (16 bytes) of lane i goes to lane j's place i.
+__device__ __forceinline__ void transpose_quad(uint32_t (&u)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 2; bit >= 1; bit >>= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = u[k * 4 + e], hi = u[(k + bit) * 4 + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+        if (up) u[k * 4 + e] = got; else u[(k + bit) * 4 + e] = got;
+      }
+    }
+  }
+}
+
+// Warps 0-7: softmax and output.
+__device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   volatile int* const abort_flag = &sm.abort_flag;
   const uint32_t slot = warp >> 2;
@@ -657,61 +747,62 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
   const int row = (warp & 3) * 32 + lane;
   const uint32_t s_t = tmem + slot * 128 + lanes, o_t = tmem + 256 + lanes;
   const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+  const uint32_t s_bar = smem_u32(&sm.s_ready[slot]), p_bar = smem_u32(&sm.p_ready[slot]);
   uint32_t own_steps = 0, other_steps = 0;   // of this slot and the other so far
-  uint32_t count = 0, items = 0, singles = 0;
+  uint32_t single_steps = 0, singles = 0;
   bool ok = true;
-  PaWalk it;
-  it.begin(a, sh);
-  for (bool first = true; ok && it.find(a, sh, first); first = false) {
-    const bool two = it.w == 2;
-    const int end0 = it.end_of_first();
-    const int x = two ? static_cast<int>(slot) : 0;                   // this thread's row tile
+  for (uint32_t count = 0;; ++count) {
+    if (!pa_item_wait<false>(sm, count, status)) break;
+    const PaItem& item = sm.items[count % kPaItems];
+    const int tokens = item.tokens;
+    if (tokens == 0) break;
+    const bool two = item.flags & kPaTwo;
+    const int j0 = item.j0, j1 = item.j1, end0 = item.end0, pre_tiles = item.pre_tiles;
     // this row: its token, and the keys that it sees
+    const int x = two ? static_cast<int>(slot) : 0;                   // this thread's row tile
     const int tok_in_item = x * a.tpt + row_tok;
-    const bool live = row_tok < a.tpt && tok_in_item < it.tokens;
-    const int64_t sees = it.run.base < 0 ? it.run.keys
-                                         : it.run.base + static_cast<int64_t>(it.i) * 2 * a.tpt + tok_in_item + 1;
+    const bool live = row_tok < a.tpt && tok_in_item < tokens;
+    const int pre_sees = item.pre, own_sees = item.sees + tok_in_item;
+    const int own_least = __shfl_sync(0xffffffffu, own_sees, 0);      // rows see more and more
     const bool warp_live = __any_sync(0xffffffffu, live);
-    const int64_t least = __shfl_sync(0xffffffffu, sees, 0);          // rows see more and more
-    const uint32_t par = count & 1;
-    int j, step, end;
-    if (two) {
-      j = it.j0;
-      step = 1;
-      end = slot == 0 ? end0 : it.j1;
-    } else {
-      j = it.j0 + ((slot ^ par) & 1);
+    const uint32_t turn = (slot ^ single_steps) & 1;                  // one row tile: which alternate key tiles
+    int j = j0, step = 1, end = slot == 0 ? end0 : j1;
+    if (!two) {
+      j = j0 + turn;
       step = 2;
-      end = it.j1;
-      count += it.j1 - it.j0;
+      end = j1;
+      single_steps += j1 - j0;
     }
     float m = -INFINITY, l = 0.f;
     bool fresh = true;
     for (; j < end; j += step) {
-      if (!pa_wait(smem_u32(&sm.s_ready[slot]), own_steps & 1, abort_flag, status)) { ok = false; break; }
+      if (!pa_wait(s_bar, own_steps & 1, abort_flag, status)) { ok = false; break; }
       if (warp_live) {
         tc_fence_after();
         float v[128];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32(s_t + k * 32, reinterpret_cast<uint32_t*>(v) + k * 32);
         tmem_ld_wait();
-        if (static_cast<int64_t>(j) * 128 + 128 > least) {
-          const int64_t left = sees - static_cast<int64_t>(j) * 128;
-          const int lim = left >= 128 ? 128 : (left < 0 ? 0 : static_cast<int>(left));
+        const bool in_pre = j < pre_tiles;
+        const int at = (in_pre ? j : j - pre_tiles) * 128;
+        const bool partly = at + 128 > (in_pre ? pre_sees : own_least);   // some key of the tile is not seen
+        if (partly) {
+          const int lim = (in_pre ? pre_sees : own_sees) - at;
 #pragma unroll
           for (int k = 0; k < 128; ++k) v[k] = k < lim ? v[k] : -INFINITY;
         }
-        float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+        float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]), t2 = max3(v[6], v[7], v[8]),
+              t3 = max3(v[9], v[10], v[11]);
 #pragma unroll
-        for (int k = 4; k < 128; k += 8) {
-          t0 = fmaxf(t0, fmaxf(v[k], v[k + 1]));
-          t1 = fmaxf(t1, fmaxf(v[k + 2], v[k + 3]));
-          if (k + 4 < 128) {
-            t2 = fmaxf(t2, fmaxf(v[k + 4], v[k + 5]));
-            t3 = fmaxf(t3, fmaxf(v[k + 6], v[k + 7]));
-          }
+        for (int k = 12; k < 124; k += 8) {
+          t0 = max3(t0, v[k], v[k + 1]);
+          t1 = max3(t1, v[k + 2], v[k + 3]);
+          t2 = max3(t2, v[k + 4], v[k + 5]);
+          t3 = max3(t3, v[k + 6], v[k + 7]);
         }
-        const float top = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+        t0 = max3(t0, v[124], v[125]);
+        t1 = max3(t1, v[126], v[127]);
+        const float top = fmaxf(m, fmaxf(max3(t0, t1, t2), t3));
         const bool raise = (top - m) * kScoreLog2 > kRaise;           // false where both are -inf
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? ex2((m - top) * kScoreLog2) : 1.f;
@@ -738,51 +829,56 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         const float mc = m == -INFINITY ? 0.f : -m * kScoreLog2;
         const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(mc, mc);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        auto weights = [&](auto poly) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t p[16];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 y = fma2(make_float2(v[k * 32 + 2 * e], v[k * 32 + 2 * e + 1]), scale, shift);
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            if (e & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
-            p[e] = cvt_bf16x2(y.x, y.y);
+            for (int e = 0; e < 16; ++e) {
+              float2 y = fma2(make_float2(v[k * 32 + 2 * e], v[k * 32 + 2 * e + 1]), scale, shift);
+              if (decltype(poly)::value && (e & 7) < kPolyPairs) {
+                y = exp2_poly(y);
+              } else {
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+              }
+              if (e & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
+              p[e] = cvt_bf16x2(y.x, y.y);
+            }
+            tmem_st16(s_t + k * 16, p);
           }
-          tmem_st16(s_t + k * 16, p);
-        }
+        };
+        // the polynomial has no -inf: tiles with unseen keys do without it
+        if (partly) weights(std::false_type{}); else weights(std::true_type{});
         sum0 = add2(sum0, sum1);
         l += sum0.x + sum0.y;
         tmem_st_wait();
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_ready[slot]));
+      if (lane == 0) mbar_arrive(p_bar);
       ++own_steps;
       fresh = false;
     }
     if (!ok) break;
-    const bool whole = it.j0 == 0 && it.j1 == it.n;
-    const bool carried = it.start < sh.s0;                            // the item began in an earlier share
     // ---- output: a row tile for each slot, or both slots' halves of one
     float f_own = 1.f, f_other = 0.f;
-    bool has_own = true, has_other = false;
+    bool has_own, has_other = false;
     const uint32_t other = slot ^ 1;
     if (two) {
-      has_own = end > it.j0;
-      other_steps += (slot == 0 ? it.j1 : end0) - it.j0;
+      has_own = end > j0;
+      other_steps += (slot == 0 ? j1 : end0) - j0;
     } else {
-      const int tiles = it.j1 - it.j0;
-      const int mine = (tiles + ((slot ^ par) & 1 ? 0 : 1)) >> 1, theirs = tiles - mine;
+      const int tiles = j1 - j0, mine = (tiles + (turn ? 0 : 1)) >> 1, theirs = tiles - mine;
       has_own = mine > 0;
       has_other = theirs > 0;
       other_steps += theirs;
       // (the item before has been read: both slots are done with its maxima too)
-      if (items > 0 && !pa_wait(smem_u32(&sm.o_free), (items - 1) & 1, abort_flag, status)) { ok = false; break; }
+      if (count > 0 && !pa_wait(smem_u32(&sm.o_free), (count - 1) & 1, abort_flag, status)) break;
       sm.ml[slot][row] = make_float2(m, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.ml_ready));
-      if (!pa_wait(smem_u32(&sm.ml_ready), singles & 1, abort_flag, status)) { ok = false; break; }
+      if (!pa_wait(smem_u32(&sm.ml_ready), singles & 1, abort_flag, status)) break;
       ++singles;
       const float2 o = sm.ml[other][row];
       const float top = fmaxf(m, o.x);
@@ -791,90 +887,113 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
       l = l * f_own + o.y * f_other;
       m = top;
     }
-    if (has_own && !pa_wait(smem_u32(&sm.pv_done[slot]), (own_steps - 1) & 1, abort_flag, status)) { ok = false; break; }
-    if (has_other && !pa_wait(smem_u32(&sm.pv_done[other]), (other_steps - 1) & 1, abort_flag, status)) { ok = false; break; }
+    if (has_own && !pa_wait(smem_u32(&sm.pv_done[slot]), (own_steps - 1) & 1, abort_flag, status)) break;
+    if (has_other && !pa_wait(smem_u32(&sm.pv_done[other]), (other_steps - 1) & 1, abort_flag, status)) break;
     tc_fence_after();
+    const int flags = item.flags;
     if (warp_live) {
       const int c0 = two ? 0 : static_cast<int>(slot) * 64, c1 = two ? 128 : c0 + 64;
-      const int tok = it.tok0 + it.i * 2 * a.tpt + tok_in_item;
-      const int head = it.g * a.group + row_head;
-      const bool direct = whole && !a.prefix_len;
+      const int64_t tok = item.tok + tok_in_item;
+      const int head = item.g * a.group + row_head;
+      const bool direct = (flags & kPaWhole) && a.mode != kPaPrefixOnce;
+      const bool spread = !direct && !(flags & kPaWhole);             // a piece: columns in blocks of 4
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float k_own = direct ? f_own * inv : f_own, k_other = direct ? f_other * inv : f_other;
       float* dst = nullptr;
-      if (!direct) {
+      uint16_t* quad[4];                                              // the rows of this lane's quad
+      uint32_t quad_live = 0;
+      if (direct) {
+        const int64_t off = tok * a.ld_out + static_cast<int64_t>(head) * kHeadDim + (lane & 3) * 8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          quad[e] = a.out + __shfl_sync(0xffffffffu, off - (lane & 3) * 8, (lane & ~3) + e) + (lane & 3) * 8;
+        quad_live = (__ballot_sync(0xffffffffu, live) >> (lane & ~3)) & 15u;
+      } else {
         float2* ml;
-        if (whole) {
-          const int64_t r = (it.b < 0 ? 0 : static_cast<int64_t>(a.n_tok) * a.h_q) + static_cast<int64_t>(tok) * a.h_q + head;
+        if (spread) {
+          const int64_t tile = (static_cast<int64_t>(blockIdx.x) * 2 + (flags & kPaCarried ? 0 : 1)) * 2 + x;
+          ml = reinterpret_cast<float2*>(a.work + a.off_ml) + tile * 128 + row;
+          dst = reinterpret_cast<float*>(a.work + a.off_o) + tile * 128 * kHeadDim + row * 4;
+        } else {
+          const int64_t r = (flags & kPaOnce ? 0 : static_cast<int64_t>(a.n_tok) * a.h_q) + tok * a.h_q + head;
           ml = reinterpret_cast<float2*>(a.work + a.off_row_ml) + r;
           dst = reinterpret_cast<float*>(a.work + a.off_row_o) + r * kHeadDim;
-        } else {
-          const int64_t r = ((static_cast<int64_t>(blockIdx.x) * 2 + (carried ? 0 : 1)) * 2 + x) * 128 + row;
-          ml = reinterpret_cast<float2*>(a.work + a.off_ml) + r;
-          dst = reinterpret_cast<float*>(a.work + a.off_o) + r * kHeadDim;
         }
         if (live && (two || slot == 0)) *ml = make_float2(m, l);
       }
-      uint16_t* const out = a.out + static_cast<int64_t>(tok) * a.ld_out + static_cast<int64_t>(head) * kHeadDim;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
-        uint32_t o[32], u[32];
-        if (has_own) tmem_ld32(o_t + slot * 128 + c, o);
-        if (has_other) tmem_ld32(o_t + other * 128 + c, u);
-        tmem_ld_wait();
+        uint32_t o[32];
         float r[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          r[e] = has_own ? __uint_as_float(o[e]) * k_own : 0.f;
-          if (has_other) r[e] = fmaf(__uint_as_float(u[e]), k_other, r[e]);
+        for (int e = 0; e < 32; ++e) r[e] = 0.f;
+        if (has_own) {
+          tmem_ld32(o_t + slot * 128 + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __uint_as_float(o[e]) * k_own;
         }
-        if (live) {
-          if (direct) {
+        if (has_other) {
+          tmem_ld32(o_t + other * 128 + c, o);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(out + c + e) =
-                  make_uint4(cvt_bf16x2(r[e], r[e + 1]), cvt_bf16x2(r[e + 2], r[e + 3]),
-                             cvt_bf16x2(r[e + 4], r[e + 5]), cvt_bf16x2(r[e + 6], r[e + 7]));
-          } else {
+          for (int e = 0; e < 32; ++e) r[e] = fmaf(__uint_as_float(o[e]), k_other, r[e]);
+        }
+        if (direct) {
+          // a lane has 64 bytes of its row; after the exchange a quad writes them for one row after another
+          uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + c + e) = make_float4(r[e], r[e + 1], r[e + 2], r[e + 3]);
-          }
+          for (int e = 0; e < 16; ++e) u[e] = cvt_bf16x2(r[2 * e], r[2 * e + 1]);
+          transpose_quad(u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((quad_live >> e) & 1)
+              *reinterpret_cast<uint4*>(quad[e] + c) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+        } else if (live) {
+          const int64_t stride = spread ? 128 * 4 : 4;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(dst + (c / 4 + e) * stride) =
+                make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
         }
       }
       tc_fence_before();
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.o_free));
-    ++items;
-    if (tid == 0 && !whole && it.j1 == it.n) {
+    if (threadIdx.x == 0 && !(flags & kPaWhole) && (flags & kPaEnds)) {
       // the item's last piece is here: what the joining kernel has to know
-      join->first = share_owner(sh.total, sh.ctas, it.start);
-      join->tok0 = it.tok0 + it.i * 2 * a.tpt;
-      join->n_tok = it.tokens;
-      join->g = it.g;
+      PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x;
+      join->first = item.first_cta;
+      join->tok = item.tok;
+      join->tokens = tokens;
+      join->g = item.g;
       join->valid = 1;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+      mbar_arrive(smem_u32(&sm.o_free));
     }
   }
 }
 
-// What is refused: reported, its rows zero (warps 10 and 11).
-__device__ __forceinline__ void pa_refuse(const PromptArgs& a, PaShared& sm) {
-  const int tid = threadIdx.x;
-  const PaShare& sh = sm.share;
+// Warp 11: what is refused is reported, its rows zero.
+__device__ __forceinline__ void pa_refuse(const PromptArgs& a) {
+  const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  const bool no_prefix = pa_prefix(a) < 0;
+  if (no_prefix && blockIdx.x == 0 && lane == 0) atomicOr(status, kDevBadInput);
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     const PaSequence s = pa_sequence(a, b);
-    if (!s.bad) continue;
-    if (tid == 320) atomicOr(status, kDevBadInput);
+    if (!s.bad && !no_prefix) continue;
+    if (s.bad && lane == 0) atomicOr(status, kDevBadInput);
     const int64_t t0 = s.tok0 < 0 ? 0 : s.tok0;
     int64_t t1 = a.cu ? a.cu[b + 1] : t0 + a.t_new;
     if (t1 > a.n_tok) t1 = a.n_tok;
     const int cols = a.h_q * (kHeadDim / 8);
-    for (int64_t e = tid - 320; e < (t1 - t0) * cols; e += kPaThreads - 320)
-      *reinterpret_cast<uint4*>(a.out + (t0 + e / cols) * a.ld_out + (e % cols) * 8) = make_uint4(0, 0, 0, 0);
+    for (int64_t t = t0; t < t1; ++t)
+      for (int e = lane; e < cols; e += 32)
+        *reinterpret_cast<uint4*>(a.out + t * a.ld_out + e * 8) = make_uint4(0, 0, 0, 0);
   }
-  if (a.prefix_len && blockIdx.x == 0 && tid == 320 && *a.prefix_len != sh.prefix) atomicOr(status, kDevBadInput);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -886,9 +1005,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   PaShared& sm = *reinterpret_cast<PaShared*>(pa_dyn + kPaTilesBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t q_s = smem_u32(pa_dyn), kv_s = q_s + 2 * kPaTileBytes;
-  uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   if (q_s & 1023u) {                     // the swizzled tiles count on it
-    if (tid == 0) atomicOr(status, kDevTimeout);
+    if (tid == 0) atomicOr(reinterpret_cast<uint32_t*>(a.work), kDevTimeout);
     return;
   }
 
@@ -904,6 +1022,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_init(smem_u32(&sm.s_ready[k]), 1);
         mbar_init(smem_u32(&sm.p_ready[k]), 4);
         mbar_init(smem_u32(&sm.pv_done[k]), 1);
+      }
+      for (int k = 0; k < kPaItems; ++k) {
+        mbar_init(smem_u32(&sm.item_full[k]), 1);
+        mbar_init(smem_u32(&sm.item_empty[k]), 10);
       }
       mbar_init(smem_u32(&sm.o_free), 8);
       mbar_init(smem_u32(&sm.ml_ready), 8);
@@ -924,29 +1046,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // Nothing of this call is read or written before the kernels ahead of it are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x)->valid = 0;
   tc_fence_before();
   pa_find_share(a, sm);
   tc_fence_after();
-  const PaShare& sh = sm.share;
   const uint32_t tmem = sm.tmem;
-  PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x;
-  if (tid == 0) join->valid = 0;
-
-  const bool work = sh.s0 < sh.s1;
 
   // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88, so that a thread of
   // the softmax holds its row of S.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if (work) pa_softmax(a, sm, tmem, join);
+    pa_softmax(a, sm, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp >= 10)
-      pa_refuse(a, sm);
-    else if (work && warp == 8)
-      pa_load(a, sm, q_s, kv_s, &tm_q, &tm_k, &tm_v, &tm_pk, &tm_pv);
-    else if (work)
-      pa_multiply(a, sm, tmem, q_s, kv_s);
+    if (warp == 8) pa_load(a, sm, q_s, kv_s, &tm_q, &tm_k, &tm_v, &tm_pk, &tm_pv);
+    if (warp == 9) pa_multiply(a, sm, tmem, q_s, kv_s);
+    if (warp == 10) pa_find_items(a, sm);
+    if (warp == 11) pa_refuse(a);
   }
   tc_fence_before();
   __syncthreads();
@@ -956,39 +1072,52 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
 // ---------------------------------------------------------------- joining pieces
 // A row's pieces (m, l, O) in order: out = sum e^(m_p - M) O_p / sum e^(m_p - M) l_p.
-// A warp holds a row, four columns a lane.
+// A thread holds kCols of its columns.
+template <int kQuads>
 struct PaJoined {
-  float m, l;
-  float4 o;
-  __device__ __forceinline__ void add(float2 ml, const float* src, int lane) {
-    if (ml.y <= 0.f) return;                     // nothing seen: O is not read
+  float m = -INFINITY, l = 0.f;
+  float4 o[kQuads];
+  __device__ __forceinline__ PaJoined() {
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // the columns src + k * stride
+  __device__ __forceinline__ void add(float2 ml, const float* src, int64_t stride) {
+    if (ml.x == -INFINITY || ml.y <= 0.f) return;          // nothing seen: O is not read
     const float top = fmaxf(m, ml.x);
     const float f = m == -INFINITY ? 0.f : ex2((m - top) * kScoreLog2);
     const float g = ex2((ml.x - top) * kScoreLog2);
-    const float4 v = *reinterpret_cast<const float4*>(src + lane * 4);
-    o.x = o.x * f + v.x * g;
-    o.y = o.y * f + v.y * g;
-    o.z = o.z * f + v.z * g;
-    o.w = o.w * f + v.w * g;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(src + k * stride);
+      o[k].x = o[k].x * f + v.x * g;
+      o[k].y = o[k].y * f + v.y * g;
+      o[k].z = o[k].z * f + v.z * g;
+      o[k].w = o[k].w * f + v.w * g;
+    }
     l = l * f + ml.y * g;
     m = top;
   }
-  __device__ __forceinline__ void pieces(const PromptArgs& a, int first, int last, int x, int row, int lane) {
+  // pieces of CTAs first .. last of row tile x, from block `quad` of 4 columns on
+  __device__ __forceinline__ void pieces(const PromptArgs& a, int first, int last, int x, int row, int quad) {
     for (int c = first; c <= last; ++c) {
-      const int64_t r = ((static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + x) * 128 + row;
-      add(reinterpret_cast<const float2*>(a.work + a.off_ml)[r],
-          reinterpret_cast<const float*>(a.work + a.off_o) + r * kHeadDim, lane);
+      const int64_t tile = (static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + x;
+      add(reinterpret_cast<const float2*>(a.work + a.off_ml)[tile * 128 + row],
+          reinterpret_cast<const float*>(a.work + a.off_o) + tile * 128 * kHeadDim + (quad * 128 + row) * 4, 128 * 4);
     }
   }
-  __device__ __forceinline__ void store(const PromptArgs& a, int tok, int head, int lane) const {
+  __device__ __forceinline__ void store(const PromptArgs& a, int64_t tok, int head, int quad) const {
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(tok) * a.ld_out + static_cast<int64_t>(head) * kHeadDim +
-                              lane * 4) =
-        make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
+    uint16_t* const dst = a.out + tok * a.ld_out + static_cast<int64_t>(head) * kHeadDim + quad * 4;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+      *reinterpret_cast<uint2*>(dst + k * 4) =
+          make_uint2(cvt_bf16x2(o[k].x * inv, o[k].y * inv), cvt_bf16x2(o[k].z * inv, o[k].w * inv));
   }
 };
 
-// Split items of packed prompts: grid (CTAs of the attention, 8), 8 warps; a block takes 32 rows.
+// Split items of packed prompts: grid (CTAs of the attention, 8), 8 warps.  A block takes 32 rows, a
+// lane for each (as they lie in the pieces), a warp 16 columns.
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -996,17 +1125,15 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   if (!j.valid) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = blockIdx.y >> 2;
-  for (int k = 0; k < 4; ++k) {
-    const int row = (blockIdx.y & 3) * 32 + k * 8 + warp;
-    const int t = row / a.group;
-    if (t >= a.tpt || x * a.tpt + t >= j.n_tok) return;
-    PaJoined s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    s.pieces(a, j.first, blockIdx.x, x, row, lane);
-    s.store(a, j.tok0 + x * a.tpt + t, j.g * a.group + row - t * a.group, lane);
-  }
+  const int row = (blockIdx.y & 3) * 32 + lane;
+  const int t = row / a.group;
+  if (t >= a.tpt || x * a.tpt + t >= j.tokens) return;
+  PaJoined<4> s;
+  s.pieces(a, j.first, blockIdx.x, x, row, warp * 4);
+  s.store(a, j.tok + x * a.tpt + t, j.g * a.group + row - t * a.group, warp * 4);
 }
 
-// Every row behind a shared prefix: its prefix's pieces, then its own keys'.  A warp a row.
+// Every row behind a prefix taken once: its prefix's pieces, then its own keys'.  A warp a row.
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1024,37 +1151,26 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   }
   const PaSequence seq = pa_sequence(a, b);
   const int t = tok - seq.tok0;
-  if (seq.bad || t < 0 || t >= seq.n) return;            // a refused sequence's rows are zero already
   const PaMeta meta = *reinterpret_cast<const PaMeta*>(a.work + kPaOffMeta);
-  PaJoined s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (seq.bad || t < 0 || t >= seq.n || meta.prefix < 0) return;   // what is refused is zero already
+  PaJoined<1> s;
   auto part = [&](const Run& run, int64_t start, int t, int64_t whole_row) {   // t: the token's place in the run
     const int i = t / (2 * a.tpt), x = (t / a.tpt) & 1;
     start += cost_before(run, i);
-    const int w = item_row_tiles(run, i);
-    const int n = static_cast<int>((item_keys(run, i, item_tokens(run, i)) + 127) / 128);
+    const int tokens = item_tokens(run, i), w = tokens > run.tpt ? 2 : 1, n = item_tiles(run, i, tokens);
     const int first = share_owner(meta.total, meta.ctas, start);
     const int last = share_owner(meta.total, meta.ctas, start + static_cast<int64_t>(w) * (n - 1));
     if (first == last)
       s.add(reinterpret_cast<const float2*>(a.work + a.off_row_ml)[whole_row],
-            reinterpret_cast<const float*>(a.work + a.off_row_o) + whole_row * kHeadDim, lane);
+            reinterpret_cast<const float*>(a.work + a.off_row_o) + whole_row * kHeadDim + lane * 4, 0);
     else
       s.pieces(a, first, last, x, (t % a.tpt) * a.group + head - g * a.group, lane);
   };
-  Run run;
-  run.tpt = a.tpt;
-  if (meta.prefix < 0) {                                 // refused: zero
-    s.store(a, tok, head, lane);
-    return;
-  }
   if (meta.prefix > 0) {
-    run.n = pa_packed_tokens(a);
-    run.base = -1;
-    run.keys = meta.prefix;
+    const Run run = pa_prefix_run(a, meta.prefix);
     part(run, run_cost(run) * g, tok, r);
   }
-  run.n = seq.n;
-  run.base = seq.base;
-  run.keys = 0;
+  const Run run = pa_own_run(a, seq, meta.prefix);
   part(run, reinterpret_cast<const int64_t*>(a.work + a.off_start)[b] + run_cost(run) * g, t,
        static_cast<int64_t>(a.n_tok) * a.h_q + r);
   s.store(a, tok, head, lane);

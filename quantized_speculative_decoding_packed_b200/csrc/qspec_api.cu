@@ -491,6 +491,9 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.tpt = 128 / group;
   a.l_max = l_max;
   a.prefix_max = with_prefix ? prefix_max : 0;
+  // A sequence's own rows fill a row tile (on average): the prefix goes ahead of its keys, in the
+  // same items, and nothing is left to join but what is split.
+  a.mode = !with_prefix ? kPaNoPrefix : (n_tok / batch * group >= kPaAheadRows ? kPaPrefixAhead : kPaPrefixOnce);
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
   const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};
@@ -506,7 +509,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   st = launch_dependent(prompt_attention_kernel, dim3(static_cast<unsigned>(grid)), kPaThreads, kPaSmemBytes, stream,
                         tq, tk, tv, tpk, tpv, a);
   if (st != QSPEC_OK) return st;
-  if (!with_prefix) return launch_dependent(prompt_join_kernel, dim3(static_cast<unsigned>(grid), 8), 256, 0, stream, a);
+  if (a.mode != kPaPrefixOnce) return launch_dependent(prompt_join_kernel, dim3(static_cast<unsigned>(grid), 8), 256, 0, stream, a);
   return launch_dependent(prefix_join_kernel, dim3(static_cast<unsigned>((n_tok * h_q + 7) / 8)), 256, 0, stream, a);
 }
 

@@ -2,7 +2,7 @@
 // __host__ __device__ functions the kernels use).  Prints "ok" and returns 0
 // when all of this holds, over ragged batches, grouped heads and grids:
 //
-//  1. floor_sum and cost_before equal their sums term by term.
+//  1. floor_sum_128 and cost_before equal their sums term by term.
 //  2. The shares cover every key tile of every item exactly once, in order.
 //  3. The pieces of an item are those of consecutive CTAs, the first and the
 //     last of which share_owner names, none of them empty.
@@ -33,11 +33,11 @@ static unsigned rnd(unsigned n) {
 }
 
 int main() {
-  for (int k = 0; k < 20000; ++k) {
-    const int64_t n = rnd(200), m = 1 + rnd(300), a = rnd(600), b = rnd(100000);
+  for (int k = 0; k < 40000; ++k) {
+    const int64_t n = rnd(k & 1 ? 200 : 20000), a = 1 + rnd(256), b = rnd(k & 2 ? 100000 : 2000000000);
     int64_t want = 0;
-    for (int64_t i = 0; i < n; ++i) want += (a * i + b) / m;
-    if (floor_sum(n, m, a, b) != want) return fail("floor_sum", n, m, a);
+    for (int64_t i = 0; i < n; ++i) want += (a * i + b) / 128;
+    if (floor_sum_128(n, a, b) != want) return fail("floor_sum_128", n, a, b);
   }
   const int groups[] = {1, 2, 3, 4, 5, 7, 8, 16, 48, 100, 128};
   const int grids[] = {1, 2, 7, 64, 148};
@@ -59,12 +59,11 @@ int main() {
           if (tokens < 1 || tokens > 2 * r.tpt) return fail("tokens", r.n, i, tokens);
           Entry e;
           e.start = pos;
-          e.w = item_row_tiles(r, i);
-          e.n = static_cast<int>((item_keys(r, i, tokens) + 127) / 128);
+          e.w = tokens > r.tpt ? 2 : 1;
+          e.n = item_tiles(r, i, tokens);
           if (e.n < 1) return fail("tiles", r.n, r.base, i);
           items.push_back(e);
           pos += static_cast<int64_t>(e.w) * e.n + kItemCost;
-          if (item_cost(r, i) != static_cast<int64_t>(e.w) * e.n + kItemCost) return fail("cost", r.n, r.base, i);
         }
         if (run_cost(r) != pos - head) return fail("run_cost", r.n, r.base, g);
       }
@@ -76,7 +75,7 @@ int main() {
       r.n = rnd(4) == 0 ? 0 : 1 + rnd(scale);
       r.tpt = tpt;
       r.base = rnd(2) ? 0 : rnd(5000);
-      r.keys = 0;
+      r.pre = trial % 5 == 0 ? 1 + trial % 7 : 0;
       all += r.n;
       runs.push_back(r);
     }
@@ -85,7 +84,7 @@ int main() {
       p.n = all;
       p.tpt = tpt;
       p.base = -1;
-      p.keys = 1 + rnd(9000);
+      p.pre = 1 + rnd(70);
       if (add(p)) return 1;
     }
     for (const Run& r : runs)

@@ -7,7 +7,7 @@ A = max_j sum_i |q_i k_ji| / sqrt(128) of its row:
   * a score is a sum of 128 exact products in fp32 (2^-24 each, taken twice, for the tensor
     cores may cut instead of round): an error of 2^-16 A in the exponent, in weight and sum: 2^-15 A W
   * the sum of weights and the weighted values over n keys in fp32:            n 2^-22 W
-  * exp2 (2^-22) and its argument (2^-24 of at most 2^7 for weights that count): 2^-16 W
+  * exp2 (2^-18) and its argument (2^-24 of at most 2^6 for weights that count): 2^-16 W
   * the output rounded to bf16:                                                2^-8 |out|
 The products of these are below 1 % of their sum.
 """
