@@ -27,7 +27,6 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
-#include <type_traits>
 
 #include "attention.cuh"
 #include "device_common.cuh"
@@ -199,15 +198,16 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
   return d;
 }
-// Of each 8 pairs of weights so many come from exp2_poly: the special function
-// unit, at 4 a cycle for each quarter of an SM, is what the softmax waits for.
-constexpr int kPolyPairs = 3;
+// One of so many pairs of weights comes from exp2_poly: the special function unit, at 4 a cycle for
+// each quarter of an SM, takes 1024 cycles for a warp's tile alone.  Cycles for the weights of a tile,
+// by the share of pairs: none 1400, an eighth 1200, a quarter 1060, three eighths 1190, half 1550.
+constexpr int kPolyEach = 4;
 
 // 2^x for x <= 2^7 without the special function unit: x = k + r with k the nearest
 // integer (by adding 1.5 x 2^23, whose last bits then hold k), 2^r by a
-// polynomial, k added to its exponent.  The polynomial is the one of degree 4
-// with the least relative error on |r| <= 1/2 (2.6e-6, from a weighted
-// least-squares fit), far below the 2^-9 of the bf16 that its result becomes.
+// polynomial, k added to its exponent.  The polynomial is the one of degree 3
+// with the least relative error on |r| <= 1/2 (7.5e-5, from a weighted
+// least-squares fit): 1/26 of half a step of the bf16 that its result becomes.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);
@@ -215,10 +215,9 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
   const float2 t = add2(x, big);
   const float2 k = add2(t, neg);
   const float2 r = fma2(k, make_float2(-1.f, -1.f), x);
-  float2 y = fma2(r, make_float2(0x1.3997d6p-7f, 0x1.3997d6p-7f), make_float2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
-  y = fma2(y, r, make_float2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
-  y = fma2(y, r, make_float2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
-  y = fma2(y, r, make_float2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+  float2 y = fma2(r, make_float2(0x1.c3f760p-5f, 0x1.c3f760p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
+  y = fma2(y, r, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
+  y = fma2(y, r, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
   y.x = __int_as_float((__float_as_int(t.x) << 23) + __float_as_int(y.x));
   y.y = __int_as_float((__float_as_int(t.y) << 23) + __float_as_int(y.y));
   return y;
@@ -824,6 +823,8 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         const int at = (in_pre ? j : j - pre_tiles) * 128;
         const bool partly = at + 128 > (in_pre ? pre_sees : own_least);   // some key of the tile is not seen
         if (partly) {
+          // (exp2_poly makes 2^-126 of -inf: nothing beside the largest weight of any row, and a row
+          // without any is known by its m)
           const int lim = (in_pre ? pre_sees : own_sees) - at;
 #pragma unroll
           for (int k = 0; k < 128; ++k) v[k] = k < lim ? v[k] : -INFINITY;
@@ -861,27 +862,23 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         const float mc = m == -INFINITY ? 0.f : -m * kScoreLog2;
         const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(mc, mc);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-        auto weights = [&](auto poly) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t p[16];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 y = fma2(make_float2(v[k * 32 + 2 * e], v[k * 32 + 2 * e + 1]), scale, shift);
-              if (decltype(poly)::value && (e & 7) < kPolyPairs) {
-                y = exp2_poly(y);
-              } else {
-                y.x = ex2(y.x);
-                y.y = ex2(y.y);
-              }
-              if (e & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
-              p[e] = cvt_bf16x2(y.x, y.y);
+          for (int e = 0; e < 16; ++e) {
+            float2 y = fma2(make_float2(v[k * 32 + 2 * e], v[k * 32 + 2 * e + 1]), scale, shift);
+            if (e % kPolyEach == 0) {
+              y = exp2_poly(y);
+            } else {
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
             }
-            tmem_st16(s_t + k * 16, p);
+            if (e & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
+            p[e] = cvt_bf16x2(y.x, y.y);
           }
-        };
-        // the polynomial has no -inf: tiles with unseen keys do without it
-        if (partly) weights(std::false_type{}); else weights(std::true_type{});
+          tmem_st16(s_t + k * 16, p);
+        }
         sum0 = add2(sum0, sum1);
         l += sum0.x + sum0.y;
         tmem_st_wait();
