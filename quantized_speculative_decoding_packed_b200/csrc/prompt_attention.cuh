@@ -18,6 +18,7 @@
 //   warp 9: tcgen05.mma: S of the next step before P V of the current one;
 //   warps 0-3, 4-7: the softmax of slots 0 and 1, a thread for each row.  A slot
 //           is a tile of S, and of O, in tensor memory; P takes S's place;
+//   warps 12-15: the output of an item, while the softmax is at the next.
 //   warp 11: clears the rows of sequences that are refused.
 // With two row tiles, each has a slot, and both use every key tile.  With one,
 // the slots take alternate key tiles and are joined at the end of the item.
@@ -37,7 +38,7 @@ namespace qspec {
 
 constexpr int kPaStages = 5;
 constexpr int kPaItems = 4;                                  // items passed on ahead
-constexpr int kPaThreads = 384;
+constexpr int kPaThreads = 512;
 constexpr int kPaTileBytes = 128 * kHeadDim * 2;             // 32 KB: a tile of Q, K or V
 constexpr float kScoreLog2 = kInvSqrtHeadDim * 1.4426950408889634f;   // scores in powers of two
 constexpr float kRaise = 8.f;
@@ -303,7 +304,7 @@ struct PaShare {
 // Barriers and small exchanges in shared memory.
 struct PaShared {
   uint64_t kv_full[kPaStages], kv_empty[kPaStages], q_full[2], q_empty[2];
-  uint64_t s_ready[2], p_ready[2], pv_done[2], o_free, ml_ready, drained;
+  uint64_t s_ready[2], p_ready[2], pv_done[2], o_free[2], ml_full[2], ml_free[2], drained;
   uint64_t item_full[kPaItems], item_empty[kPaItems];
   PaItem items[kPaItems];
   PaShare share;
@@ -579,7 +580,7 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_v, 0);
   bool ok = true, have = false, begun = false;   // nx is taken; its first S is issued
   PaSteps nx;
-  uint32_t count = 0, items = 0;             // items taken, begun
+  uint32_t count = 0, items0 = 0, items1 = 0;   // items taken, items with steps in slots 0 and 1
   uint32_t ring = 0, qn = 0, singles = 0;    // key tiles x 2, query tiles, steps of items with one row tile
   uint32_t p_count = 0;                      // phases of p_ready: slot 0 in bit 0, slot 1 in bit 1
   auto take = [&](bool block) -> bool {      // the next item into nx
@@ -687,12 +688,10 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
       return min(left, 128);
     };
     ring += 2 * (it.j1 - it.j0);
-    bool o_waited = items == 0;
-    const uint32_t o_phase = (items - 1) & 1;
-    ++items;
-    auto o_wait = [&]() -> bool {            // the item before has read its O
-      if (!o_waited) ok = pa_wait(smem_u32(&sm.o_free), o_phase, abort_flag, status);
-      o_waited = true;
+    // the item before with steps in the slot has read its O
+    auto o_wait = [&](uint32_t slot) -> bool {
+      const uint32_t before = slot ? items1++ : items0++;
+      if (before > 0) ok = ok && pa_wait(smem_u32(&sm.o_free[slot]), (before - 1) & 1, abort_flag, status);
       return ok;
     };
     if (it.two) {
@@ -709,12 +708,14 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
         const uint32_t r = r0 + 2 * j;
         const bool more0 = j + 1 < it.end0, more1 = j + 1 < it.j1;
         const int tail = tail_of(j);
-        if (!o_wait() || !wait_kv(r + 1)) break;
+        if (!wait_kv(r + 1)) break;
+        if (j == it.j0 && has0 && !o_wait(0)) break;
         if (j < it.end0 && !values(0, r + 1, tail, j == it.j0, false, !more0)) break;
         bool next_k = more0 && landed(r + 2);
         if (next_k) scores(0, q0, r + 2, false, j + 2 >= it.end0);
         const bool issued0 = next_k;
         if (!more1) begin_next(0, ring, qn);
+        if (j == it.j0 && !o_wait(1)) break;
         if (!values(1, r + 1, tail, j == it.j0, true, !more1)) break;
         if (more1) {
           if (!next_k && !wait_kv(r + 2)) break;
@@ -736,7 +737,7 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
         const bool early = more && landed(r + 2);
         if (early) scores(slot ^ 1, q, r + 2, true, j + 2 >= it.j1);
         if (!more) begin_next(slot ^ 1, ring, qn);
-        if (!o_wait() || !wait_kv(r + 1)) break;
+        if (!wait_kv(r + 1) || (j < it.j0 + 2 && !o_wait(slot))) break;
         if (!values(slot, r + 1, tail_of(j), j < it.j0 + 2, true, j + 2 >= it.j1)) break;
         if (more && !early) {
           if (!wait_kv(r + 2)) break;
@@ -772,7 +773,7 @@ __device__ __forceinline__ void transpose_quad(uint32_t (&u)[16]) {
   }
 }
 
-// Warps 0-7: softmax and output.
+// Warps 0-7: the softmax.
 __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
@@ -780,12 +781,12 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
   const uint32_t slot = warp >> 2;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // lane base of this warp, in bits 16..
   const int row = (warp & 3) * 32 + lane;
-  const uint32_t s_t = tmem + slot * 128 + lanes, o_t = tmem + 256 + lanes;
-  const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+  const uint32_t s_t = tmem + slot * 128 + lanes, o_t = tmem + 256 + slot * 128 + lanes;
+  const int row_tok = row / a.group;
   const uint32_t s_bar = smem_u32(&sm.s_ready[slot]), p_bar = smem_u32(&sm.p_ready[slot]);
   uint32_t own_steps = 0;                    // of this slot so far
-  uint32_t own_items = 0, other_items = 0;   // items with steps in this slot, in the other
-  uint32_t single_steps = 0, singles = 0;
+  uint32_t own_items = 0;                    // items with steps in this slot
+  uint32_t single_steps = 0;
   bool ok = true;
   for (uint32_t count = 0;; ++count) {
     if (!pa_item_wait(sm, count, status)) break;
@@ -801,6 +802,8 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
     const int pre_sees = item.pre, own_sees = item.sees + tok_in_item;
     const int own_least = __shfl_sync(0xffffffffu, own_sees, 0);      // rows see more and more
     const bool warp_live = __any_sync(0xffffffffu, live);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
     const uint32_t turn = (slot ^ single_steps) & 1;                  // one row tile: which alternate key tiles
     int j = j0, step = 1, end = slot == 0 ? end0 : j1;
     if (!two) {
@@ -809,6 +812,7 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
       end = j1;
       single_steps += j1 - j0;
     }
+    if (j >= end) continue;                                           // no key tile for this slot
     float m = -INFINITY, l = 0.f;
     bool fresh = true;
     for (; j < end; j += step) {
@@ -851,11 +855,11 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
 #pragma unroll 1
             for (int k = 0; k < 128; k += 16) {
               uint32_t o[16];
-              tmem_ld16(o_t + slot * 128 + k, o);
+              tmem_ld16(o_t + k, o);
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(o_t + slot * 128 + k, o);
+              tmem_st16(o_t + k, o);
             }
           }
         }
@@ -890,118 +894,146 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
       fresh = false;
     }
     if (!ok) break;
-    // ---- output: a row tile for each slot, or both slots' halves of one
-    float f_own = 1.f, f_other = 0.f;
-    bool has_own, has_other = false;
-    const uint32_t other = slot ^ 1;
-    if (two) {
-      has_own = end > j0;
-      other_items += (slot == 0 ? j1 : end0) > j0;
-    } else {
-      const int tiles = j1 - j0, mine = (tiles + (turn ? 0 : 1)) >> 1, theirs = tiles - mine;
-      has_own = mine > 0;
-      has_other = theirs > 0;
-      other_items += has_other;
-      // (the item before has been read: both slots are done with its maxima too)
-      if (count > 0 && !pa_wait(smem_u32(&sm.o_free), (count - 1) & 1, abort_flag, status)) break;
-      sm.ml[slot][row] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.ml_ready));
-      if (!pa_wait(smem_u32(&sm.ml_ready), singles & 1, abort_flag, status)) break;
-      ++singles;
-      const float2 o = sm.ml[other][row];
-      const float top = fmaxf(m, o.x);
-      f_own = m == -INFINITY ? 0.f : ex2((m - top) * kScoreLog2);
-      f_other = o.x == -INFINITY ? 0.f : ex2((o.x - top) * kScoreLog2);
-      l = l * f_own + o.y * f_other;
-      m = top;
-    }
-    own_items += has_own;
-    if (has_own && !pa_wait(smem_u32(&sm.pv_done[slot]), (own_items - 1) & 1, abort_flag, status)) break;
-    if (has_other && !pa_wait(smem_u32(&sm.pv_done[other]), (other_items - 1) & 1, abort_flag, status)) break;
-    tc_fence_after();
-    const int flags = item.flags;
-    if (warp_live) {
-      const int c0 = two ? 0 : static_cast<int>(slot) * 64, c1 = two ? 128 : c0 + 64;
-      const int64_t tok = item.tok + tok_in_item;
-      const int head = item.g * a.group + row_head;
-      const bool direct = (flags & kPaWhole) && a.mode != kPaPrefixOnce;
-      const bool spread = !direct && !(flags & kPaWhole);             // a piece: columns in blocks of 4
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float k_own = direct ? f_own * inv : f_own, k_other = direct ? f_other * inv : f_other;
-      float* dst = nullptr;
-      uint16_t* quad[4];                                              // the rows of this lane's quad
-      uint32_t quad_live = 0;
-      if (direct) {
-        const int64_t off = tok * a.ld_out + static_cast<int64_t>(head) * kHeadDim + (lane & 3) * 8;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          quad[e] = a.out + __shfl_sync(0xffffffffu, off - (lane & 3) * 8, (lane & ~3) + e) + (lane & 3) * 8;
-        quad_live = (__ballot_sync(0xffffffffu, live) >> (lane & ~3)) & 15u;
-      } else {
-        float2* ml;
-        if (spread) {
-          const int64_t tile = (static_cast<int64_t>(blockIdx.x) * 2 + (flags & kPaCarried ? 0 : 1)) * 2 + x;
-          ml = reinterpret_cast<float2*>(a.work + a.off_ml) + tile * 128 + row;
-          dst = reinterpret_cast<float*>(a.work + a.off_o) + tile * 128 * kHeadDim + row * 4;
-        } else {
-          const int64_t r = (flags & kPaOnce ? 0 : static_cast<int64_t>(a.n_tok) * a.h_q) + tok * a.h_q + head;
-          ml = reinterpret_cast<float2*>(a.work + a.off_row_ml) + r;
-          dst = reinterpret_cast<float*>(a.work + a.off_row_o) + r * kHeadDim;
-        }
-        if (live && (two || slot == 0)) *ml = make_float2(m, l);
-      }
-#pragma unroll 1
-      for (int c = c0; c < c1; c += 32) {
-        uint32_t o[32];
-        float r[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = 0.f;
-        if (has_own) {
-          tmem_ld32(o_t + slot * 128 + c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __uint_as_float(o[e]) * k_own;
-        }
-        if (has_other) {
-          tmem_ld32(o_t + other * 128 + c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = fmaf(__uint_as_float(o[e]), k_other, r[e]);
-        }
-        if (direct) {
-          // a lane has 64 bytes of its row; after the exchange a quad writes them for one row after another
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = cvt_bf16x2(r[2 * e], r[2 * e + 1]);
-          transpose_quad(u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((quad_live >> e) & 1)
-              *reinterpret_cast<uint4*>(quad[e] + c) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-        } else if (live) {
-          const int64_t stride = spread ? 128 * 4 : 4;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4*>(dst + (c / 4 + e) * stride) =
-                make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-        }
-      }
-      tc_fence_before();
-    }
-    if (threadIdx.x == 0 && !(flags & kPaWhole) && (flags & kPaEnds)) {
+    // the maximum and the sum, for the output (which has taken the last ones)
+    if (own_items > 0 && !pa_wait(smem_u32(&sm.ml_free[slot]), (own_items - 1) & 1, abort_flag, status)) break;
+    ++own_items;
+    sm.ml[slot][row] = make_float2(m, l);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.ml_full[slot]));
+  }
+}
+
+// Warps 12-15: the output, a thread for each row.  O is read as soon as its last product is done, and
+// given back for the next item's; the softmax is then already at that one.
+__device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uint32_t tmem) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  volatile int* const abort_flag = &sm.abort_flag;
+  const uint32_t o_t = tmem + 256 + (static_cast<uint32_t>(warp) << 21);
+  const int row = warp * 32 + lane;
+  const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+  uint32_t items0 = 0, items1 = 0, single_steps = 0;   // items with steps in slots 0 and 1
+  for (uint32_t count = 0;; ++count) {
+    if (!pa_item_wait(sm, count, status)) return;
+    const PaItem item = sm.items[count % kPaItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+    if (item.tokens == 0) return;
+    const bool two = item.flags & kPaTwo;
+    const int tiles = item.j1 - item.j0;
+    const bool has0 = two ? item.end0 > item.j0 : (single_steps & 1) == 0 || tiles > 1;
+    const bool has1 = two ? true : (single_steps & 1) == 1 || tiles > 1;
+    if (!two) single_steps += tiles;
+    const uint32_t phase0 = items0 & 1, phase1 = items1 & 1;
+    items0 += has0;
+    items1 += has1;
+    if (!(item.flags & kPaWhole) && (item.flags & kPaEnds) && threadIdx.x == kPaThreads - 128) {
       // the item's last piece is here: what the joining kernel has to know
       PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x;
       join->first = item.first_cta;
       join->tok = item.tok;
-      join->tokens = tokens;
+      join->tokens = item.tokens;
       join->g = item.g;
       join->valid = 1;
     }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
-      mbar_arrive(smem_u32(&sm.o_free));
+    // a row tile for each slot, or one row tile from both slots
+    for (int x = 0; x < (two ? 2 : 1); ++x) {
+      const bool use0 = has0 && x == 0, use1 = has1 && (x == 1 || !two);
+      float2 ml0 = make_float2(-INFINITY, 0.f), ml1 = ml0;
+      if (use0) {
+        if (!pa_wait(smem_u32(&sm.ml_full[0]), phase0, abort_flag, status)) return;
+        ml0 = sm.ml[0][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.ml_free[0]));
+      }
+      if (use1) {
+        if (!pa_wait(smem_u32(&sm.ml_full[1]), phase1, abort_flag, status)) return;
+        ml1 = sm.ml[1][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.ml_free[1]));
+      }
+      const float m = fmaxf(ml0.x, ml1.x);
+      float f0 = ml0.x == -INFINITY ? 0.f : ex2((ml0.x - m) * kScoreLog2);
+      float f1 = ml1.x == -INFINITY ? 0.f : ex2((ml1.x - m) * kScoreLog2);
+      const float l = ml0.y * f0 + ml1.y * f1;
+      const int tok_in_item = x * a.tpt + row_tok;
+      const bool live = row_tok < a.tpt && tok_in_item < item.tokens;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int64_t tok = item.tok + tok_in_item;
+      const int head = item.g * a.group + row_head;
+      const bool whole = item.flags & kPaWhole;
+      const bool direct = whole && a.mode != kPaPrefixOnce;
+      float* dst = nullptr;
+      uint16_t* quad[4];                                              // the rows of this lane's quad
+      uint32_t quad_live = 0;
+      if (direct) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+        const int64_t off = tok * a.ld_out + static_cast<int64_t>(head) * kHeadDim;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) quad[e] = a.out + __shfl_sync(0xffffffffu, off, (lane & ~3) + e) + (lane & 3) * 8;
+        quad_live = (__ballot_sync(0xffffffffu, live) >> (lane & ~3)) & 15u;
+      } else {
+        float2* ml;
+        if (!whole) {                                                 // a piece: columns in blocks of 4
+          const int64_t tile = (static_cast<int64_t>(blockIdx.x) * 2 + (item.flags & kPaCarried ? 0 : 1)) * 2 + x;
+          ml = reinterpret_cast<float2*>(a.work + a.off_ml) + tile * 128 + row;
+          dst = reinterpret_cast<float*>(a.work + a.off_o) + tile * 128 * kHeadDim + row * 4;
+        } else {
+          const int64_t r = (item.flags & kPaOnce ? 0 : static_cast<int64_t>(a.n_tok) * a.h_q) + tok * a.h_q + head;
+          ml = reinterpret_cast<float2*>(a.work + a.off_row_ml) + r;
+          dst = reinterpret_cast<float*>(a.work + a.off_row_o) + r * kHeadDim;
+        }
+        if (live) *ml = make_float2(m, l);
+      }
+      if (use0 && !pa_wait(smem_u32(&sm.pv_done[0]), phase0, abort_flag, status)) return;
+      if (use1 && !pa_wait(smem_u32(&sm.pv_done[1]), phase1, abort_flag, status)) return;
+      tc_fence_after();
+      if (warp_live && (use0 || use1)) {
+        const int stride = whole ? 4 : 128 * 4;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float r[32];
+          if (use0 && use1) {
+            uint32_t o[32], u[32];
+            tmem_ld32(o_t + c, o);
+            tmem_ld32(o_t + 128 + c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = fmaf(__uint_as_float(o[e]), f0, __uint_as_float(u[e]) * f1);
+          } else {
+            uint32_t o[32];
+            tmem_ld32(o_t + (use0 ? 0 : 128) + c, o);
+            tmem_ld_wait();
+            const float f = use0 ? f0 : f1;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __uint_as_float(o[e]) * f;
+          }
+          if (direct) {
+            // a lane has 64 bytes of its row; after the exchange a quad writes them for one row after another
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = cvt_bf16x2(r[2 * e], r[2 * e + 1]);
+            transpose_quad(u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((quad_live >> e) & 1)
+                *reinterpret_cast<uint4*>(quad[e] + c) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(dst + (c / 4 + e) * stride) =
+                  make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (use0) mbar_arrive(smem_u32(&sm.o_free[0]));
+        if (use1) mbar_arrive(smem_u32(&sm.o_free[1]));
+      }
     }
   }
 }
@@ -1052,13 +1084,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_init(smem_u32(&sm.s_ready[k]), 1);
         mbar_init(smem_u32(&sm.p_ready[k]), 4);
         mbar_init(smem_u32(&sm.pv_done[k]), 1);
+        mbar_init(smem_u32(&sm.o_free[k]), 4);
+        mbar_init(smem_u32(&sm.ml_full[k]), 4);
+        mbar_init(smem_u32(&sm.ml_free[k]), 4);
       }
       for (int k = 0; k < kPaItems; ++k) {
         mbar_init(smem_u32(&sm.item_full[k]), 1);
-        mbar_init(smem_u32(&sm.item_empty[k]), 10);
+        mbar_init(smem_u32(&sm.item_empty[k]), 14);
       }
-      mbar_init(smem_u32(&sm.o_free), 8);
-      mbar_init(smem_u32(&sm.ml_ready), 8);
       mbar_init(smem_u32(&sm.drained), 1);
       sm.abort_flag = 0;
       fence_barrier_init();
@@ -1082,13 +1115,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  // Registers: 384 x 168 at launch = 256 x 192 + 128 x 120, so that a thread of
+  // Registers: 512 x 128 at launch = 256 x 160 + 256 x 96, so that a thread of
   // the softmax holds its row of S.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     pa_softmax(a, sm, tmem);
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    pa_output(a, sm, tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 8) pa_load(a, sm, q_s, kv_s, &tm_q, &tm_k, &tm_v, &tm_pk, &tm_pv);
     if (warp == 9) pa_multiply(a, sm, tmem, q_s, kv_s);
     if (warp == 10) pa_find_items(a, sm);
