@@ -569,75 +569,217 @@ __device__ __forceinline__ void pa_load(const PromptArgs& a, PaShared& sm, uint3
 // instructions take are kept visibly the same for the whole warp (uniform registers), and P V is
 // committed for the softmax at the end of the item alone: S of the same slot comes after it, and S's
 // commit says that it is done.
-struct PaSteps {                       // what this warp keeps of an item
-  int tokens, j0, j1, end0, pre_tiles, pre, last_sees;
-  bool two;
-};
+// Each kind of product stands in the code once: the roles of the warps share the instruction caches, and
+// what runs once an item is read from afar each time (with ten copies a short item took 12000 cycles).
 __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, uint32_t tmem_v, uint32_t q_s, uint32_t kv_s) {
   const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   volatile int* const abort_flag = &sm.abort_flag;
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_v, 0);
-  bool ok = true, have = false, begun = false;   // nx is taken; its first S is issued
-  PaSteps nx;
-  uint32_t count = 0, items0 = 0, items1 = 0;   // items taken, items with steps in slots 0 and 1
+  bool ok = true, more = true, in_item = false;
+  // the item at hand
+  int j0 = 0, j1 = 0, end0 = 0, pre_tiles = 0, pre = 0, last_sees = 0;
+  bool two = false, has0 = false;
+  uint32_t count = 0;                        // items taken
   uint32_t ring = 0, qn = 0, singles = 0;    // key tiles x 2, query tiles, steps of items with one row tile
+  // the next S: its slot, whether its queries and keys are not known to have landed
+  int j = 0;
+  uint32_t slot = 0, q = 0;
+  bool have_s = false, new_q = false, new_k = false;
+  // P V to come, in order: ring place of the values, tail | flags
+  uint32_t pv_r[2] = {0, 0}, pv_w[2] = {0, 0}, ahead = 0, busy = 0;
+  constexpr uint32_t kSlot = 256, kFirst = 512, kFree = 1024, kLast = 2048, kNew = 4096;
   uint32_t p_count = 0;                      // phases of p_ready: slot 0 in bit 0, slot 1 in bit 1
-  auto take = [&](bool block) -> bool {      // the next item into nx
-    if (have) return true;
-    const uint32_t bar = smem_u32(&sm.item_full[count % kPaItems]), ph = (count / kPaItems) & 1;
-    if (block) {
-      if (!pa_wait(bar, ph, abort_flag, status)) { ok = false; return false; }
-    } else if (!__all_sync(0xffffffffu, mbar_test_wait(bar, ph))) {
-      return false;
-    }
-    const int mine = lane < 12 ? reinterpret_cast<const int32_t*>(&sm.items[count % kPaItems])[lane] : 0;
-    nx.tokens = __shfl_sync(0xffffffffu, mine, 1);
-    nx.j0 = __shfl_sync(0xffffffffu, mine, 4);
-    nx.j1 = __shfl_sync(0xffffffffu, mine, 5);
-    nx.end0 = __shfl_sync(0xffffffffu, mine, 6);
-    nx.pre_tiles = __shfl_sync(0xffffffffu, mine, 7);
-    nx.pre = __shfl_sync(0xffffffffu, mine, 8);
-    nx.last_sees = __shfl_sync(0xffffffffu, mine, 9) + nx.tokens - 1;
-    nx.two = __shfl_sync(0xffffffffu, mine, 10) & kPaTwo;
-    if (elect_one_lane()) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
-    ++count;
-    have = true;
-    return true;
-  };
-  auto landed = [&](uint32_t r) -> bool {
-    return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sm.kv_full[r % kPaStages]), (r / kPaStages) & 1));
-  };
-  auto wait_kv = [&](uint32_t r) -> bool {
-    ok = ok && pa_wait(smem_u32(&sm.kv_full[r % kPaStages]), (r / kPaStages) & 1, abort_flag, status);
-    return ok;
-  };
-  auto wait_q = [&](uint32_t q) -> bool {
-    ok = ok && pa_wait(smem_u32(&sm.q_full[q & 1]), (q >> 1) & 1, abort_flag, status);
-    return ok;
-  };
-  // S of query tile q with the key tile in ring place r (both landed)
-  auto scores = [&](uint32_t slot, uint32_t q, uint32_t r, bool free_k, bool free_q) {
-    const uint64_t q_desc = smem_desc_sw128(q_s + (q & 1) * kPaTileBytes);
-    const uint64_t k_desc = smem_desc_sw128(kv_s + (r % kPaStages) * kPaTileBytes);
-    if (elect_one_lane()) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = ((k >> 2) * (kPaTileBytes / 2) + (k & 3) * 32) >> 4;
-        mma_ss_bf16(tmem + slot * 128, q_desc + off, k_desc + off, kIdescScores, k > 0);
+  uint32_t o_count[2] = {0, 0};              // items with steps in the slots
+  while (ok) {
+    if (!have_s && more) {
+      if (!in_item) {
+        const uint32_t bar = smem_u32(&sm.item_full[count % kPaItems]), ph = (count / kPaItems) & 1;
+        bool got = __all_sync(0xffffffffu, mbar_test_wait(bar, ph));
+        if (!got && ahead == 0) {
+          ok = got = pa_wait(bar, ph, abort_flag, status);
+          if (!ok) break;
+        }
+        if (got) {
+          const int mine = lane < 12 ? reinterpret_cast<const int32_t*>(&sm.items[count % kPaItems])[lane] : 0;
+          const int tokens = __shfl_sync(0xffffffffu, mine, 1);
+          j0 = __shfl_sync(0xffffffffu, mine, 4);
+          j1 = __shfl_sync(0xffffffffu, mine, 5);
+          end0 = __shfl_sync(0xffffffffu, mine, 6);
+          pre_tiles = __shfl_sync(0xffffffffu, mine, 7);
+          pre = __shfl_sync(0xffffffffu, mine, 8);
+          last_sees = __shfl_sync(0xffffffffu, mine, 9) + tokens - 1;
+          two = __shfl_sync(0xffffffffu, mine, 10) & kPaTwo;
+          if (elect_one_lane()) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+          ++count;
+          more = tokens != 0;
+          in_item = more;
+          has0 = two && end0 > j0;
+          j = j0;
+          slot = two ? (has0 ? 0 : 1) : singles & 1;
+          q = qn;
+          new_q = new_k = true;
+        }
       }
-      mma_commit(smem_u32(&sm.s_ready[slot]));
-      if (free_k) mma_commit(smem_u32(&sm.kv_empty[r % kPaStages]));
-      if (free_q) mma_commit(smem_u32(&sm.q_empty[q & 1]));
+      have_s = in_item;
     }
-    __syncwarp();
-  };
-  // O (+)= P V with the value tile in ring place r (landed); tail: the tile's first unseen key (128: none)
-  auto values = [&](uint32_t slot, uint32_t r, int tail, bool first, bool free_v, bool last) -> bool {
+    if (have_s && ahead < 2 && !((busy >> slot) & 1)) {
+      const uint32_t kb = smem_u32(&sm.kv_full[ring % kPaStages]), kp = (ring / kPaStages) & 1;
+      const uint32_t qb = smem_u32(&sm.q_full[q & 1]), qp = (q >> 1) & 1;
+      bool ready = (!new_q || __all_sync(0xffffffffu, mbar_test_wait(qb, qp))) &&
+                   (!new_k || __all_sync(0xffffffffu, mbar_test_wait(kb, kp)));
+      if (!ready && ahead == 0) {
+        ok = ready = pa_wait(qb, qp, abort_flag, status) && pa_wait(kb, kp, abort_flag, status);
+        if (!ok) break;
+      }
+      if (ready) {
+        // the last step on this key tile, and on these queries
+        const bool free_k = !two || slot == 1, free_q = two && slot == 0 ? j + 1 == end0 : j + 1 == j1;
+        const uint64_t q_desc = smem_desc_sw128(q_s + (q & 1) * kPaTileBytes);
+        const uint64_t k_desc = smem_desc_sw128(kv_s + (ring % kPaStages) * kPaTileBytes);
+        if (elect_one_lane()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = ((k >> 2) * (kPaTileBytes / 2) + (k & 3) * 32) >> 4;
+            mma_ss_bf16(tmem + slot * 128, q_desc + off, k_desc + off, kIdescScores, k > 0);
+          }
+          mma_commit(smem_u32(&sm.s_ready[slot]));
+          if (free_k) mma_commit(smem_u32(&sm.kv_empty[ring % kPaStages]));
+          if (free_q) mma_commit(smem_u32(&sm.q_empty[q & 1]));
+        }
+        __syncwarp();
+        const int left = j < pre_tiles ? pre - j * 128 : last_sees - (j - pre_tiles) * 128;
+        const bool first = j == j0 || (!two && j == j0 + 1);
+        const bool last = two ? free_q : j + 2 >= j1;
+        const uint32_t w = static_cast<uint32_t>(min(left, 128)) | (slot ? kSlot : 0) | (first ? kFirst : 0) |
+                           (free_k ? kFree : 0) | (last ? kLast : 0) | (new_k ? kNew : 0);
+        if (ahead == 0) {
+          pv_r[0] = ring + 1;
+          pv_w[0] = w;
+        } else {
+          pv_r[1] = ring + 1;
+          pv_w[1] = w;
+        }
+        ++ahead;
+        busy |= 1u << slot;
+        // the next step
+        have_s = false;
+        new_k = free_k;
+        if (two && slot == 0) {
+          slot = 1;
+          q = qn + 1;
+          new_q = j == j0;
+        } else {
+          ring += 2;
+          new_q = false;
+          if (++j >= j1) {
+            in_item = false;
+            qn += has0 ? 2 : 1;
+            if (!two) singles += j1 - j0;
+          } else if (two) {
+            slot = j < end0 ? 0 : 1;
+            q = qn + (slot == 1 && has0);
+          } else {
+            slot ^= 1;
+          }
+        }
+        if (ahead < 2) continue;
+      }
+    }
+    if (ahead == 0) {
+      if (more) continue;
+      break;
+    }
+    if (two && in_item && ahead == 2 && slot == 0 && !(pv_w[0] & (kFirst | kSlot))) {
+      // The middle of an item with two row tiles, all keys seen: nothing to decide but whether the keys
+      // are there.  P V of tile j - 1 and S of tile j, for slot 0, then for slot 1.
+      bool landed = true;
+      // A barrier is looked at, and a fence made, while the last two products before are still queued.
+      const uint32_t p0 = smem_u32(&sm.p_ready[0]), p1 = smem_u32(&sm.p_ready[1]);
+      bool p_there = false;                    // P of the slot at hand is known (and fenced)
+      while (j + 1 < end0 && (j - 1 >= pre_tiles || j * 128 <= pre)) {
+        const uint32_t k_st = ring % kPaStages, v_st = (ring - 1) % kPaStages;
+        const uint32_t kb = smem_u32(&sm.kv_full[k_st]), kp = (ring / kPaStages) & 1;
+        const uint64_t k_desc = smem_desc_sw128(kv_s + k_st * kPaTileBytes);
+        const uint64_t v_desc = smem_desc_rows_n(kv_s + v_st * kPaTileBytes);
+        if (!pa_wait(smem_u32(&sm.kv_full[v_st]), ((ring - 1) / kPaStages) & 1, abort_flag, status)) { ok = false; break; }
+#pragma unroll 1
+        for (uint32_t x = 0; x < 2; ++x) {
+          if (!p_there) {
+            if (!pa_wait(x ? p1 : p0, (p_count >> x) & 1, abort_flag, status)) { ok = false; break; }
+            tc_fence_after();
+          }
+          p_there = false;
+          p_count ^= 1u << x;
+          const uint64_t q_desc = smem_desc_sw128(q_s + ((qn + x) & 1) * kPaTileBytes);
+          if (elect_one_lane()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts<false>(tmem + 256 + x * 128, tmem + x * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues, 1);
+            if (x) mma_commit(smem_u32(&sm.kv_empty[v_st]));
+          }
+          __syncwarp();
+          if (x == 0) {
+            landed = __all_sync(0xffffffffu, mbar_test_wait(kb, kp));
+            if (!landed) break;
+          }
+          if (elect_one_lane()) {
+#pragma unroll
+            for (int k = 0; k < 6; ++k) {
+              const uint32_t off = ((k >> 2) * (kPaTileBytes / 2) + (k & 3) * 32) >> 4;
+              mma_ss_bf16(tmem + x * 128, q_desc + off, k_desc + off, kIdescScores, k > 0);
+            }
+          }
+          __syncwarp();
+          p_there = __all_sync(0xffffffffu, mbar_test_wait(x ? p0 : p1, (p_count >> (x ^ 1)) & 1));
+          if (p_there) tc_fence_after();
+          if (elect_one_lane()) {
+#pragma unroll
+            for (int k = 6; k < 8; ++k) {
+              const uint32_t off = ((k >> 2) * (kPaTileBytes / 2) + (k & 3) * 32) >> 4;
+              mma_ss_bf16(tmem + x * 128, q_desc + off, k_desc + off, kIdescScores, 1);
+            }
+            mma_commit(smem_u32(&sm.s_ready[x]));
+            if (x) mma_commit(smem_u32(&sm.kv_empty[k_st]));
+          }
+          __syncwarp();
+        }
+        if (!ok || !landed) break;
+        ++j;
+        ring += 2;
+        pv_r[0] = pv_r[1] = ring - 1;
+        pv_w[0] = 128 | kNew;
+        pv_w[1] = 128 | kSlot | kFree;
+      }
+      if (!ok) break;
+      if (!landed) {                           // P V of slot 0 is done, that of slot 1 is to come
+        pv_r[0] = pv_r[1];
+        pv_w[0] = pv_w[1];
+        ahead = 1;
+        busy = 2;
+        new_k = true;
+        pv_w[0] &= ~kNew;
+        continue;
+      }
+    }
+    // O (+)= P V of the oldest S
+    const uint32_t r = pv_r[0], w = pv_w[0];
+    pv_r[0] = pv_r[1];
+    pv_w[0] = pv_w[1];
+    --ahead;
+    const uint32_t ps = w & kSlot ? 1 : 0;
+    const int tail = w & 255;                // the tile's first unseen key (128: none)
+    const uint32_t vb = smem_u32(&sm.kv_full[r % kPaStages]);
+    if ((w & kNew) && !pa_wait(vb, (r / kPaStages) & 1, abort_flag, status)) { ok = false; break; }
     const uint32_t va = kv_s + (r % kPaStages) * kPaTileBytes;
+    if (w & kFirst) {                        // the item before with steps in the slot has read its O
+      const uint32_t before = ps ? o_count[1]++ : o_count[0]++;
+      if (before > 0 && !pa_wait(smem_u32(&sm.o_free[ps]), (before - 1) & 1, abort_flag, status)) { ok = false; break; }
+    }
     const int pv_steps = (tail + 15) >> 4;
     if (tail & 15) {
       // keys past the last one seen may hold anything: their weights are 0, their values are made 0
+#pragma unroll 1
       for (int e = lane; e < (pv_steps * 16 - tail) * 16; e += 32) {
         const uint32_t at = va + ((e >> 3) & 1) * (kPaTileBytes / 2) + (tail + (e >> 4)) * 128 + (e & 7) * 16;
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
@@ -645,106 +787,21 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
       fence_proxy_async_smem();
       __syncwarp();
     }
-    ok = pa_wait(smem_u32(&sm.p_ready[slot]), (p_count >> slot) & 1, abort_flag, status);
-    if (!ok) return false;
-    p_count ^= 1u << slot;
+    if (!pa_wait(smem_u32(&sm.p_ready[ps]), (p_count >> ps) & 1, abort_flag, status)) { ok = false; break; }
+    p_count ^= 1u << ps;
     tc_fence_after();
     const uint64_t v_desc = smem_desc_rows_n(va);
     if (elect_one_lane()) {
-      if (pv_steps == 8) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts<false>(tmem + 256 + slot * 128, tmem + slot * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues,
-                        !(first && k == 0));
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < pv_steps; ++k)
-          mma_ts<false>(tmem + 256 + slot * 128, tmem + slot * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues,
-                        !(first && k == 0));
-      }
-      if (free_v) mma_commit(smem_u32(&sm.kv_empty[r % kPaStages]));
-      if (last) mma_commit(smem_u32(&sm.pv_done[slot]));
+      for (int k = 0; k < 8; ++k)
+        if (k < pv_steps)
+          mma_ts<false>(tmem + 256 + ps * 128, tmem + ps * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues,
+                        k > 0 || !(w & kFirst));
+      if (w & kFree) mma_commit(smem_u32(&sm.kv_empty[r % kPaStages]));
+      if (w & kLast) mma_commit(smem_u32(&sm.pv_done[ps]));
     }
     __syncwarp();
-    return true;
-  };
-  // S of the first step of the next item, where it is that of the free `slot` and all it takes has landed
-  auto begin_next = [&](uint32_t slot, uint32_t r, uint32_t q) {
-    if (!take(false) || nx.tokens == 0) return;
-    if (nx.two ? slot != 0 || nx.end0 <= nx.j0 : slot != (singles & 1)) return;
-    if (!__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sm.q_full[q & 1]), (q >> 1) & 1)) || !landed(r)) return;
-    scores(slot, q, r, !nx.two, (nx.two ? nx.end0 : nx.j1) - nx.j0 == 1);
-    begun = true;
-  };
-  while (ok) {
-    if (!take(true) || nx.tokens == 0) break;
-    have = false;
-    const PaSteps it = nx;
-    const bool was_begun = begun;
-    begun = false;
-    const uint32_t r0 = ring - 2 * it.j0;    // + 2 j: the ring place of key tile j
-    auto tail_of = [&](int j) -> int {
-      const int left = j < it.pre_tiles ? it.pre - j * 128 : it.last_sees - (j - it.pre_tiles) * 128;
-      return min(left, 128);
-    };
-    ring += 2 * (it.j1 - it.j0);
-    // the item before with steps in the slot has read its O
-    auto o_wait = [&](uint32_t slot) -> bool {
-      const uint32_t before = slot ? items1++ : items0++;
-      if (before > 0) ok = ok && pa_wait(smem_u32(&sm.o_free[slot]), (before - 1) & 1, abort_flag, status);
-      return ok;
-    };
-    if (it.two) {
-      const bool has0 = it.end0 > it.j0;
-      const uint32_t q0 = qn, q1 = qn + (has0 ? 1 : 0);
-      qn = q1 + 1;
-      if (has0 && !was_begun) {
-        if (!wait_q(q0) || !wait_kv(r0 + 2 * it.j0)) break;
-        scores(0, q0, r0 + 2 * it.j0, false, it.end0 - it.j0 == 1);
-      }
-      if (!wait_q(q1) || (!has0 && !wait_kv(r0 + 2 * it.j0))) break;
-      scores(1, q1, r0 + 2 * it.j0, true, it.j1 - it.j0 == 1);
-      for (int j = it.j0; j < it.j1; ++j) {
-        const uint32_t r = r0 + 2 * j;
-        const bool more0 = j + 1 < it.end0, more1 = j + 1 < it.j1;
-        const int tail = tail_of(j);
-        if (!wait_kv(r + 1)) break;
-        if (j == it.j0 && has0 && !o_wait(0)) break;
-        if (j < it.end0 && !values(0, r + 1, tail, j == it.j0, false, !more0)) break;
-        bool next_k = more0 && landed(r + 2);
-        if (next_k) scores(0, q0, r + 2, false, j + 2 >= it.end0);
-        const bool issued0 = next_k;
-        if (!more1) begin_next(0, ring, qn);
-        if (j == it.j0 && !o_wait(1)) break;
-        if (!values(1, r + 1, tail, j == it.j0, true, !more1)) break;
-        if (more1) {
-          if (!next_k && !wait_kv(r + 2)) break;
-          if (more0 && !issued0) scores(0, q0, r + 2, false, j + 2 >= it.end0);
-          scores(1, q1, r + 2, true, j + 2 >= it.j1);
-        }
-      }
-    } else {
-      const uint32_t q = qn++;
-      const uint32_t par = singles;
-      singles += it.j1 - it.j0;
-      if (!was_begun) {
-        if (!wait_q(q) || !wait_kv(r0 + 2 * it.j0)) break;
-        scores(par & 1, q, r0 + 2 * it.j0, true, it.j1 - it.j0 == 1);
-      }
-      for (int j = it.j0; j < it.j1; ++j) {
-        const uint32_t r = r0 + 2 * j, slot = (par + j - it.j0) & 1;
-        const bool more = j + 1 < it.j1;
-        const bool early = more && landed(r + 2);
-        if (early) scores(slot ^ 1, q, r + 2, true, j + 2 >= it.j1);
-        if (!more) begin_next(slot ^ 1, ring, qn);
-        if (!wait_kv(r + 1) || (j < it.j0 + 2 && !o_wait(slot))) break;
-        if (!values(slot, r + 1, tail_of(j), j < it.j0 + 2, true, j + 2 >= it.j1)) break;
-        if (more && !early) {
-          if (!wait_kv(r + 2)) break;
-          scores(slot ^ 1, q, r + 2, true, j + 2 >= it.j1);
-        }
-      }
-    }
+    busy &= ~(1u << ps);
   }
   if (!ok) {
     // given up: the products in flight end before tensor memory goes
@@ -819,59 +876,61 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
       if (!pa_wait(s_bar, own_steps & 1, abort_flag, status)) { ok = false; break; }
       if (warp_live) {
         tc_fence_after();
-        float v[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s_t + k * 32, reinterpret_cast<uint32_t*>(v) + k * 32);
-        tmem_ld_wait();
         const bool in_pre = j < pre_tiles;
         const int at = (in_pre ? j : j - pre_tiles) * 128;
         const bool partly = at + 128 > (in_pre ? pre_sees : own_least);   // some key of the tile is not seen
+        const int lim = (in_pre ? pre_sees : own_sees) - at;
         if (partly) {
-          // (exp2_poly makes 2^-126 of -inf: nothing beside the largest weight of any row, and a row
-          // without any is known by its m)
-          const int lim = (in_pre ? pre_sees : own_sees) - at;
+          // the tile's unseen keys, in tensor memory (a small loop for what is rare: the warps of all roles
+          // share the instruction caches).  exp2_poly makes 2^-126 of -inf: nothing beside the largest
+          // weight of any row, and a row without any is known by its m.
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            if (!__any_sync(0xffffffffu, c + 16 > lim)) continue;
+            uint32_t x[16];
+            tmem_ld16(s_t + c, x);
+            tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 128; ++k) v[k] = k < lim ? v[k] : -INFINITY;
+            for (int e = 0; e < 16; ++e) x[e] = c + e < lim ? x[e] : 0xff800000u;
+            tmem_st16(s_t + c, x);
+          }
+          tmem_st_wait();
         }
-        float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]), t2 = max3(v[6], v[7], v[8]),
-              t3 = max3(v[9], v[10], v[11]);
+        // S is read twice, 32 columns at a time, in loops that stay small
+        uint32_t u[2][32];
+        float top = m;
+        auto largest = [&](const uint32_t* x) {
+          float t[2] = {top, -INFINITY};
 #pragma unroll
-        for (int k = 12; k < 124; k += 8) {
-          t0 = max3(t0, v[k], v[k + 1]);
-          t1 = max3(t1, v[k + 2], v[k + 3]);
-          t2 = max3(t2, v[k + 4], v[k + 5]);
-          t3 = max3(t3, v[k + 6], v[k + 7]);
+          for (int e = 0; e < 32; e += 2) t[(e >> 1) & 1] = max3(t[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          top = fmaxf(t[0], t[1]);
+        };
+        tmem_ld32(s_t, u[0]);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          tmem_ld_wait();
+          tmem_ld32(s_t + c + 32, u[1]);
+          largest(u[0]);
+          tmem_ld_wait();
+          if (c == 0) tmem_ld32(s_t + 64, u[0]);
+          largest(u[1]);
         }
-        t0 = max3(t0, v[124], v[125]);
-        t1 = max3(t1, v[126], v[127]);
-        const float top = fmaxf(m, fmaxf(max3(t0, t1, t2), t3));
+        tmem_ld32(s_t, u[0]);
         const bool raise = (top - m) * kScoreLog2 > kRaise;           // false where both are -inf
+        float f = 1.f;
         if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? ex2((m - top) * kScoreLog2) : 1.f;
+          f = raise ? ex2((m - top) * kScoreLog2) : 1.f;
           l *= f;
           if (raise) m = top;
-          if (!fresh) {
-            // what O holds so far is for the old maximum (P V of the step before is done: S came after it)
-#pragma unroll 1
-            for (int k = 0; k < 128; k += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_t + k, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(o_t + k, o);
-            }
-          }
         }
         const float mc = m == -INFINITY ? 0.f : -m * kScoreLog2;
         const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(mc, mc);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        auto weights = [&](const uint32_t* x, int c) {
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 y = fma2(make_float2(v[k * 32 + 2 * e], v[k * 32 + 2 * e + 1]), scale, shift);
+            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale, shift);
             if (e % kPolyEach == 0) {
               y = exp2_poly(y);
             } else {
@@ -881,7 +940,28 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
             if (e & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
             p[e] = cvt_bf16x2(y.x, y.y);
           }
-          tmem_st16(s_t + k * 16, p);
+          tmem_st16(s_t + (c >> 1), p);       // over S columns that have been read
+        };
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          tmem_ld_wait();
+          tmem_ld32(s_t + c + 32, u[1]);
+          weights(u[0], c);
+          tmem_ld_wait();
+          if (c == 0) tmem_ld32(s_t + 64, u[0]);
+          weights(u[1], c + 32);
+        }
+        if (!fresh && __any_sync(0xffffffffu, f != 1.f)) {
+          // what O holds so far is for the old maximum (P V of the step before is done: S came after it)
+#pragma unroll 1
+          for (int k = 0; k < 128; k += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_t + k, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_t + k, o);
+          }
         }
         sum0 = add2(sum0, sum1);
         l += sum0.x + sum0.y;
