@@ -444,6 +444,39 @@ def kv_commit(lens: torch.Tensor, n_accepted: torch.Tensor, l_max: int,
 
 
 # ---------------------------------------------------------------- the prompt path
+# These calls run thousands of times a second for single tokens, so what they do on the host
+# is kept short: the current stream is asked for as a plain handle (3 us less than the Stream
+# object), pointers go to the library as integers.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """The address of a contiguous tensor of `dtype` on CUDA device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}, "
+                         f"not {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, dtype, dev: int, rows: int, columns: int, name: str) -> int:
+    """The address of a [rows][>= columns] tensor with unit column stride."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a {dtype} tensor [tokens][columns] with unit column stride on cuda:{dev}")
+    if t.shape[0] != rows or t.shape[1] < columns:
+        raise ValueError(f"{name} must be [{rows}][{columns}], not {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _current_device(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
 # Default workspaces of the prompt attention, by device and stream: calls on two
 # streams have two.  One that has become too small is kept, for a captured graph may
 # still write to it.
@@ -451,30 +484,38 @@ _PROMPT_WS: dict = {}
 _PROMPT_WS_RETIRED: list = []
 
 
-def _new_prompt_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+def _new_prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        ws[:PROMPT_WORKSPACE_ZERO].zero_()
     return ws
 
 
-def prompt_workspace(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
+PROMPT_WORKSPACE_ZERO = 16384     # bytes of a prompt attention workspace that start as zeros
+
+
+def prompt_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     """A scratch buffer of at least `nbytes` bytes for the prompt attention calls on one stream.
 
     Under stream capture the buffer belongs to the graph alone.  Graphs that share a buffer
     passed as `work` must not run at the same time.
     """
+    dev = torch.device(device).index if torch.device(device).index is not None else torch.cuda.current_device()
+    return _prompt_workspace(nbytes, dev, _raw_stream(dev) if stream is None else stream.cuda_stream)
+
+
+def _prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
-        return _new_prompt_workspace(nbytes, device)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    key = (device, s.cuda_stream)
-    cur = _PROMPT_WS.get(key)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        ws[:PROMPT_WORKSPACE_ZERO].zero_()
+        return ws
+    cur = _PROMPT_WS.get((dev, handle))
     if cur is None or cur.numel() < nbytes:
         if cur is not None:
             _PROMPT_WS_RETIRED.append(cur)
             nbytes = max(nbytes, 2 * cur.numel())
-        with torch.cuda.stream(s):
-            cur = _new_prompt_workspace(nbytes, device)
-        _PROMPT_WS[key] = cur
+        cur = _new_prompt_workspace(nbytes, dev, handle)
+        _PROMPT_WS[(dev, handle)] = cur
     return cur
 
 
@@ -484,62 +525,56 @@ _PREFILL_WS_SIZE: dict = {}
 def attn_prefill_workspace_size() -> int:
     """Bytes that attn_prefill needs on the current device (0 where it does not run)."""
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    if dev not in _PREFILL_WS_SIZE:
-        _PREFILL_WS_SIZE[dev] = int(LIB.qspec_attn_prefill_workspace_size())
-    return _PREFILL_WS_SIZE[dev]
+    size = _PREFILL_WS_SIZE.get(dev)
+    if size is None:
+        size = _PREFILL_WS_SIZE[dev] = int(LIB.qspec_attn_prefill_workspace_size())
+    return size
 
 
 def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int) -> int:
     return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q))
 
 
-def _tokens_check(t: torch.Tensor, dtype, name: str):
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor [tokens][columns] with unit column stride")
+def _cache_on(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int):
+    """(addresses, batch, KV heads, positions) of a cache pair."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != HEAD_DIM:
+        raise ValueError("k_cache and v_cache must both be [B][H_kv][L_max][128]")
+    b, h_kv, l_max, _ = k_cache.shape
+    return _on(k_cache, _BF16, dev, "k_cache"), _on(v_cache, _BF16, dev, "v_cache"), b, h_kv, l_max
 
 
-def _packed_check(cu, lens: torch.Tensor, batch: int, n_tokens: int, columns: int, needed: int, name: str) -> None:
-    _need(lens, torch.int32, "lens")
+def _packed_on(cu, lens: torch.Tensor, batch: int, n_tokens: int, dev: int):
+    """Addresses of lens and cu (None: the same number of tokens for every sequence)."""
     if lens.numel() != batch:
         raise ValueError(f"lens has {lens.numel()} entries for a cache of {batch} sequences")
-    if cu is not None:
-        _need(cu, torch.int32, "cu")
-        if cu.numel() != batch + 1:
-            raise ValueError(f"cu has {cu.numel()} entries, {batch + 1} are needed")
-    elif n_tokens == 0 or n_tokens % batch != 0:
-        raise ValueError(f"{name} has {n_tokens} rows, not a positive multiple of the batch {batch}")
-    if columns < needed:
-        raise ValueError(f"{name} has {columns} columns, {needed} are needed")
+    if cu is None:
+        if n_tokens == 0 or n_tokens % batch != 0:
+            raise ValueError(f"{n_tokens} rows are not a positive multiple of the batch {batch}")
+        return _on(lens, _I32, dev, "lens"), None
+    if cu.numel() != batch + 1:
+        raise ValueError(f"cu has {cu.numel()} entries, {batch + 1} are needed")
+    return _on(lens, _I32, dev, "lens"), _on(cu, _I32, dev, "cu")
 
 
-def _prefix_len_check(prefix_len) -> None:
-    _need(prefix_len, torch.int32, "prefix_len")
-    if prefix_len.numel() != 1:
+def _one(t: torch.Tensor, dev: int) -> int:
+    if t.numel() != 1:
         raise ValueError("prefix_len must have one element")
-
-
-def _same_device(*tensors) -> None:
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one device: {t.device} and {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return _on(t, _I32, dev, "prefix_len")
 
 
 def rope_table(inv_freq: torch.Tensor, positions: int, table: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """Angles of `positions` positions for qkv_rope_append: inv_freq fp64 [rot/2] -> fp32 [positions][rot],
     cosines, then sines (computed in 64 bits)."""
-    _need(inv_freq, torch.float64, "inv_freq")
+    dev = _current_device(inv_freq)
     rot = 2 * inv_freq.numel()
+    freq = _on(inv_freq, torch.float64, dev, "inv_freq")
     if table is None:
-        table = torch.empty((positions, rot), dtype=torch.float32, device=inv_freq.device)
-    _need(table, torch.float32, "table")
+        table = torch.empty((positions, rot), dtype=_F32, device=inv_freq.device)
     if tuple(table.shape) != (positions, rot):
         raise ValueError(f"table must be [{positions}][{rot}]")
-    _same_device(inv_freq, table)
-    _check(LIB.qspec_rope_table(_ptr(inv_freq), rot, positions, _ptr(table), _stream(stream)), "qspec_rope_table")
+    _check(LIB.qspec_rope_table(freq, rot, positions, _on(table, _F32, dev, "table"),
+                                _raw_stream(dev) if stream is None else stream.cuda_stream), "qspec_rope_table")
     return table
 
 
@@ -555,45 +590,34 @@ def qkv_rope_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache:
     table: rope_table's, or None for no rotation.  cu: int32 [batch + 1] starts of the sequences' tokens
     (None: the same number for each).
     """
-    _qkv_check(qkv)
-    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
-    n, cols = qkv.shape
-    _packed_check(cu, lens, b, n, cols, (h_q + 2 * h_kv) * HEAD_DIM, "qkv")
+    dev = _current_device(qkv)
+    kc, vc, b, h_kv, l_max = _cache_on(k_cache, v_cache, dev)
+    n = qkv.shape[0]
+    x = _rows(qkv, _F32, dev, n, (h_q + 2 * h_kv) * HEAD_DIM, "qkv")
+    lens_p, cu_p = _packed_on(cu, lens, b, n, dev)
     rot = positions = 0
+    angles = None
     if table is not None:
-        _need(table, torch.float32, "table")
         positions, rot = table.shape
-    for gamma, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        angles = _on(table, _F32, dev, "table")
+    gammas = [None, None]
+    for i, gamma in enumerate((q_gamma, k_gamma)):
         if gamma is not None:
-            _need(gamma, torch.float32, name)
             if gamma.numel() != HEAD_DIM:
-                raise ValueError(f"{name} must have {HEAD_DIM} entries")
-    if prefix_len is not None:
-        _prefix_len_check(prefix_len)
+                raise ValueError(f"q_gamma and k_gamma must have {HEAD_DIM} entries")
+            gammas[i] = _on(gamma, _F32, dev, "q_gamma" if i == 0 else "k_gamma")
     if q_out is None:
-        q_out = torch.empty((n, h_q * HEAD_DIM), dtype=torch.bfloat16, device=qkv.device)
-    if q_out.dtype not in (torch.bfloat16, torch.float32):
+        q_out = torch.empty((n, h_q * HEAD_DIM), dtype=_BF16, device=qkv.device)
+    if q_out.dtype is not _BF16 and q_out.dtype is not _F32:
         raise ValueError("q_out must be bf16 or fp32")
-    _tokens_check(q_out, q_out.dtype, "q_out")
-    if q_out.shape[0] != n or q_out.shape[1] < h_q * HEAD_DIM:
-        raise ValueError(f"q_out must be [{n}][{h_q * HEAD_DIM}]")
-    _same_device(qkv, lens, k_cache, v_cache, table, cu, prefix_len, q_gamma, k_gamma, q_out, work)
-    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_Q_FP32 if q_out.dtype == torch.float32 else 0)
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_Q_FP32 if q_out.dtype is _F32 else 0)
     _check(LIB.qspec_qkv_rope_append(
-        _ptr(qkv), qkv.stride(0), n, b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(q_gamma), _ptr(k_gamma), eps,
-        _ptr(table), positions, rot, _ptr(prefix_len), _ptr(lens), offset, _ptr(k_cache), _ptr(v_cache), l_max,
-        _ptr(q_out), q_out.stride(0), flags, _ptr(work), 0 if work is None else work.numel(), _stream(stream)),
-        "qspec_qkv_rope_append")
+        x, qkv.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM, gammas[0], gammas[1], eps, angles, positions, rot,
+        None if prefix_len is None else _one(prefix_len, dev), lens_p, offset, kc, vc, l_max,
+        _rows(q_out, q_out.dtype, dev, n, h_q * HEAD_DIM, "q_out"), q_out.stride(0), flags,
+        None if work is None else _on(work, torch.uint8, dev, "work"), 0 if work is None else work.numel(),
+        _raw_stream(dev) if stream is None else stream.cuda_stream), "qspec_qkv_rope_append")
     return q_out
-
-
-def _prompt_out(q: torch.Tensor, h_q: int, out):
-    if out is None:
-        return torch.empty((q.shape[0], h_q * HEAD_DIM), dtype=torch.bfloat16, device=q.device)
-    _tokens_check(out, torch.bfloat16, "out")
-    if out.shape[0] != q.shape[0] or out.shape[1] < h_q * HEAD_DIM:
-        raise ValueError(f"out must be [{q.shape[0]}][{h_q * HEAD_DIM}]")
-    return out
 
 
 def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -604,18 +628,20 @@ def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache:
     Token i of sequence b (rows cu[b] .. cu[b + 1] - 1 of q) sees positions 0 .. lens[b] + i.  Rows behind the
     last sequence are not written.
     """
-    _tokens_check(q, torch.bfloat16, "q")
-    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
+    dev = _current_device(q)
     if cu is None:
         raise ValueError("cu is needed")
-    _packed_check(cu, lens, b, q.shape[0], q.shape[1], h_q * HEAD_DIM, "q")
-    out = _prompt_out(q, h_q, out)
-    _same_device(q, cu, lens, k_cache, v_cache, out, work)
+    kc, vc, b, h_kv, l_max = _cache_on(k_cache, v_cache, dev)
+    n, cols = q.shape[0], h_q * HEAD_DIM
+    lens_p, cu_p = _packed_on(cu, lens, b, n, dev)
+    if out is None:
+        out = torch.empty((n, cols), dtype=_BF16, device=q.device)
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = prompt_workspace(attn_prefill_workspace_size(), q.device, stream)
-    _check(LIB.qspec_attn_prefill(_ptr(q), q.stride(0), q.shape[0], b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(lens),
-                                  _ptr(k_cache), _ptr(v_cache), l_max, _ptr(out), out.stride(0), _ptr(work),
-                                  work.numel(), _stream(stream)), "qspec_attn_prefill")
+        work = _prompt_workspace(attn_prefill_workspace_size(), dev, handle)
+    _check(LIB.qspec_attn_prefill(_rows(q, _BF16, dev, n, cols, "q"), q.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM,
+                                  lens_p, kc, vc, l_max, _rows(out, _BF16, dev, n, cols, "out"), out.stride(0),
+                                  _on(work, torch.uint8, dev, "work"), work.numel(), handle), "qspec_attn_prefill")
     return out
 
 
@@ -629,20 +655,20 @@ def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
     positions 0 .. lens[b] + offset + t of its own cache.  cu None: the same number of tokens for each sequence
     (drafting and verifying passes); else packed prompts.
     """
-    _tokens_check(q, torch.bfloat16, "q")
-    b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
-    _packed_check(cu, lens, b, q.shape[0], q.shape[1], h_q * HEAD_DIM, "q")
-    _need(prefix_k, torch.bfloat16, "prefix_k")
-    _need(prefix_v, torch.bfloat16, "prefix_v")
+    dev = _current_device(q)
+    kc, vc, b, h_kv, l_max = _cache_on(k_cache, v_cache, dev)
+    n, cols = q.shape[0], h_q * HEAD_DIM
+    lens_p, cu_p = _packed_on(cu, lens, b, n, dev)
     if prefix_k.dim() != 3 or prefix_k.shape != prefix_v.shape or prefix_k.shape[0] != h_kv or prefix_k.shape[2] != HEAD_DIM:
         raise ValueError(f"prefix_k and prefix_v must both be [{h_kv}][positions][{HEAD_DIM}]")
-    _prefix_len_check(prefix_len)
-    out = _prompt_out(q, h_q, out)
-    _same_device(q, cu, lens, k_cache, v_cache, prefix_k, prefix_v, prefix_len, out, work)
+    if out is None:
+        out = torch.empty((n, cols), dtype=_BF16, device=q.device)
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = prompt_workspace(attn_prefix_workspace_size(q.shape[0], b, h_q), q.device, stream)
-    _check(LIB.qspec_attn_prefix(_ptr(q), q.stride(0), q.shape[0], b, _ptr(cu), h_q, h_kv, HEAD_DIM, _ptr(lens),
-                                 offset, _ptr(k_cache), _ptr(v_cache), l_max, _ptr(prefix_k), _ptr(prefix_v),
-                                 prefix_k.shape[1], _ptr(prefix_len), _ptr(out), out.stride(0), _ptr(work),
-                                 work.numel(), _stream(stream)), "qspec_attn_prefix")
+        work = _prompt_workspace(attn_prefix_workspace_size(n, b, h_q), dev, handle)
+    _check(LIB.qspec_attn_prefix(_rows(q, _BF16, dev, n, cols, "q"), q.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM,
+                                 lens_p, offset, kc, vc, l_max, _on(prefix_k, _BF16, dev, "prefix_k"),
+                                 _on(prefix_v, _BF16, dev, "prefix_v"), prefix_k.shape[1], _one(prefix_len, dev),
+                                 _rows(out, _BF16, dev, n, cols, "out"), out.stride(0),
+                                 _on(work, torch.uint8, dev, "work"), work.numel(), handle), "qspec_attn_prefix")
     return out
