@@ -296,9 +296,8 @@ enum : int { kPaTwo = 1, kPaWhole = 2, kPaCarried = 4, kPaEnds = 8, kPaOnce = 16
 
 struct PaShare {
   int64_t s0, s1, total;
-  int64_t start;               // of the first item
-  int b, g, i;                 // the first item; b < 0: the prefix's
-  int ctas, prefix;
+  int64_t start;               // of the sequence in which the share begins
+  int b, ctas;                 // b < 0: the prefix
 };
 
 // Barriers and small exchanges in shared memory.
@@ -309,8 +308,6 @@ struct PaShared {
   PaItem items[kPaItems];
   PaShare share;
   int64_t warp_sums[kPaThreads / 32];
-  int64_t found_start, found_cost;
-  int found_b;
   int abort_flag;
   uint32_t tmem;
   float2 ml[2][128];
@@ -319,21 +316,50 @@ constexpr int kPaTilesBytes = (2 + kPaStages) * kPaTileBytes;          // Q, K a
 constexpr int kPaSmemBytes = kPaTilesBytes + static_cast<int>(sizeof(PaShared));
 static_assert(kPaSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-// The costs of all sequences, their sum, and this CTA's first item.
+// The last item of a run starting at `start` that starts at or before s0: [lo, lo + n) narrowed 32-fold
+// by a warp; `at`: where it starts.
+__device__ __noinline__ int64_t pa_cost_before(int n, int tpt, int base, int pre, int i) {
+  Run r;
+  r.n = n;
+  r.tpt = tpt;
+  r.base = base;
+  r.pre = pre;
+  return cost_before(r, i);
+}
+__device__ __forceinline__ int64_t pa_run_cost(const Run& r) {
+  return r.n > 0 ? pa_cost_before(r.n, r.tpt, r.base, r.pre, run_items(r)) : 0;
+}
+__device__ __forceinline__ int pa_find_item(const Run& r, int64_t start, int64_t s0, int64_t* at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = run_items(r);
+  int64_t found = start;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int64_t mine = start + (lane * step < n ? pa_cost_before(r.n, r.tpt, r.base, r.pre, lo + lane * step) : 0);
+    const bool le = lane * step < n && (lane == 0 || mine <= s0);
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    found = __shfl_sync(0xffffffffu, mine, k);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  *at = found;
+  return lo;
+}
+
+constexpr int kPaWarpBatch = 64;     // up to so many sequences one warp finds the shares alone
+
+// More sequences than that: the whole CTA sums their costs, and finds the one in which its share begins.
 __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int prefix = pa_prefix(a);
-  const Run pr = pa_prefix_run(a, prefix);
-  const int64_t prefix_head = run_cost(pr);
-  const int64_t prefix_all = prefix_head * a.h_kv;
-
+  const int64_t prefix_all = pa_run_cost(pa_prefix_run(a, prefix)) * a.h_kv;
   int64_t before = prefix_all;         // the cost before the chunk of sequences at hand
   int64_t cost = 0, at = 0;            // of one KV head of this thread's sequence; before the sequence
   auto scan = [&](int b) {
-    cost = b < a.batch ? run_cost(pa_own_run(a, pa_sequence(a, b), prefix)) : 0;
+    cost = b < a.batch ? pa_run_cost(pa_own_run(a, pa_sequence(a, b), prefix)) : 0;
     const int64_t mine = cost * a.h_kv;
     int64_t incl = mine;
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += o;
@@ -342,86 +368,132 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
     __syncthreads();
     int64_t all = 0;
     at = before + incl - mine;
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < kPaThreads / 32; ++k) {
       const int64_t s = sm.warp_sums[k];
       if (k < warp) at += s;
       all += s;
     }
     before += all;
-    if (a.batch > kPaThreads) __syncthreads();   // the sums are written again
+    __syncthreads();                   // the sums are written again
   };
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) scan(b0 + tid);
   const int64_t total = before;
-  const int ctas = working_ctas(total, gridDim.x);
-  const int c = blockIdx.x;
-  const int64_t s0 = c < ctas ? share_start(total, ctas, c) : total;
-  const int64_t s1 = c < ctas ? share_start(total, ctas, c + 1) : total;
+  const int ctas = working_ctas(total, gridDim.x), c = blockIdx.x;
+  int64_t s0 = total, s1 = total;
+  if (c < ctas && total > 0) share_of(total, ctas, c, &s0, &s1);
   if (tid == 0) {
     sm.share.s0 = s0;
     sm.share.s1 = s1;
     sm.share.total = total;
     sm.share.ctas = ctas;
-    sm.share.prefix = prefix;
-    if (c == 0) {
-      PaMeta* meta = reinterpret_cast<PaMeta*>(a.work + kPaOffMeta);
-      meta->total = total;
-      meta->ctas = ctas;
-      meta->prefix = prefix;
-    }
+    sm.share.b = -1;
+    sm.share.start = 0;
   }
+  __syncthreads();
   int64_t* const starts = a.mode == kPaPrefixOnce ? reinterpret_cast<int64_t*>(a.work + a.off_start) : nullptr;
   before = prefix_all;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
     const int b = b0 + tid;
     if (a.batch > kPaThreads) scan(b);           // else this thread's values still stand
     if (b < a.batch) {
       if (c == 0 && starts) starts[b] = at;
       if (cost > 0 && at <= s0 && s0 < at + cost * a.h_kv) {
-        sm.found_b = b;
-        sm.found_start = at;
-        sm.found_cost = cost;
+        sm.share.b = b;
+        sm.share.start = at;
       }
     }
   }
   __syncthreads();
-  if (s0 < s1 && warp == 10) {
-    int b = -1;
-    int64_t start = 0, head_cost = prefix_head;
-    Run r = pr;
-    if (s0 >= prefix_all) {
-      b = sm.found_b;
-      start = sm.found_start;
-      head_cost = sm.found_cost;
-      r = pa_own_run(a, pa_sequence(a, b), prefix);
-    }
-    const int g = static_cast<int>(div_u64(s0 - start, head_cost));
-    start += g * head_cost;
-    // the last item that starts at or before s0: [lo, lo + n) narrowed 32-fold
-    int lo = 0, n = run_items(r);
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const bool le = lane * step < n && (lane == 0 || start + cost_before(r, lo + lane * step) <= s0);
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
-    if (lane == 0) {
-      sm.share.b = b;
-      sm.share.g = g;
-      sm.share.i = lo;
-      sm.share.start = start + cost_before(r, lo);
-    }
-  }
 }
 
 // ---------------------------------------------------------------- the roles of the warps
 // Warp 10: the share's items in order, into the ring.
 __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm) {
   const int lane = threadIdx.x & 31;
-  __syncwarp();
-  const PaShare sh = sm.share;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  const int prefix = pa_prefix(a);
+  const Run prefix_run = pa_prefix_run(a, prefix);
+  const int64_t prefix_head = pa_run_cost(prefix_run);
+  PaSequence mine;               // of sequence block * 32 + lane
+  int b = -1, block = -1;
+  int64_t total, s0, s1, start = 0, head_cost = prefix_head;
+  int ctas;
+  auto load = [&](int at) {
+    if (at == block) return;
+    block = at;
+    mine.n = 0;
+    if (block * 32 + lane < a.batch) mine = pa_sequence(a, block * 32 + lane);
+  };
+  auto own_run = [&](int of) -> Run {
+    PaSequence s;
+    s.n = __shfl_sync(0xffffffffu, mine.n, of & 31);
+    s.base = __shfl_sync(0xffffffffu, mine.base, of & 31);
+    return pa_own_run(a, s, prefix);
+  };
+  if (a.batch <= kPaWarpBatch) {
+    // every lane: the cost of a sequence, or of two; then which of them the share begins in
+    int64_t cost[2] = {0, 0}, at[2] = {0, 0};
+    total = prefix_head * a.h_kv;
+#pragma unroll 1
+    for (int half = 1; half >= 0; --half) {       // the first 32 last: they stay in `mine`
+      if (half * 32 >= a.batch) continue;
+      load(half);
+      const int64_t one = pa_run_cost(pa_own_run(a, mine, prefix));
+      int64_t incl = one * a.h_kv;
+#pragma unroll 1
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      if (half == 0) {
+        cost[0] = one;
+        at[0] = prefix_head * a.h_kv + incl - one * a.h_kv;
+        const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
+        at[1] += prefix_head * a.h_kv + sum;
+        total += sum;
+      } else {
+        cost[1] = one;
+        at[1] = incl - one * a.h_kv;
+        total += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    ctas = working_ctas(total, gridDim.x);
+    s0 = s1 = total;
+    if (blockIdx.x < ctas && total > 0) share_of(total, ctas, blockIdx.x, &s0, &s1);
+    const uint32_t in0 = __ballot_sync(0xffffffffu, cost[0] > 0 && at[0] <= s0 && s0 < at[0] + cost[0] * a.h_kv);
+    const uint32_t in1 = __ballot_sync(0xffffffffu, cost[1] > 0 && at[1] <= s0 && s0 < at[1] + cost[1] * a.h_kv);
+    if (in0 | in1) {
+      const int of = __ffs(in0 ? in0 : in1) - 1;
+      b = of + (in0 ? 0 : 32);
+      start = __shfl_sync(0xffffffffu, in0 ? at[0] : at[1], of);
+      head_cost = __shfl_sync(0xffffffffu, in0 ? cost[0] : cost[1], of);
+    }
+    if (blockIdx.x == 0 && a.mode == kPaPrefixOnce) {
+      int64_t* const starts = reinterpret_cast<int64_t*>(a.work + a.off_start);
+      if (lane < a.batch) starts[lane] = at[0];
+      if (lane + 32 < a.batch) starts[lane + 32] = at[1];
+    }
+  } else {
+    total = sm.share.total;
+    ctas = sm.share.ctas;
+    s0 = sm.share.s0;
+    s1 = sm.share.s1;
+    b = sm.share.b;
+    start = sm.share.start;
+    if (b >= 0) {
+      load(b >> 5);
+      head_cost = pa_run_cost(own_run(b));
+    }
+  }
+  if (blockIdx.x == 0 && lane == 0) {
+    PaMeta* meta = reinterpret_cast<PaMeta*>(a.work + kPaOffMeta);
+    meta->total = total;
+    meta->ctas = ctas;
+    meta->prefix = prefix;
+  }
   uint32_t count = 0;
   auto pass = [&](const PaItem& it) -> bool {
     const uint32_t slot = count % kPaItems;
@@ -435,33 +507,28 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
     return true;
   };
   PaItem it;
-  if (sh.s0 < sh.s1) {
-    int b = sh.b, g = sh.g, i = sh.i, block = -1;
-    int64_t start = sh.start;
-    PaSequence mine;             // of sequence block * 32 + lane
-    mine.n = mine.tok0 = mine.base = 0;
-    Run run = pa_prefix_run(a, sh.prefix);
-    int tok0 = 0;
-    auto load = [&]() {          // sequence b's run
-      if ((b >> 5) != block) {
-        block = b >> 5;
-        if (block * 32 + lane < a.batch) mine = pa_sequence(a, block * 32 + lane);
-        else mine.n = 0;
-      }
-      PaSequence s;
-      s.n = __shfl_sync(0xffffffffu, mine.n, b & 31);
-      s.tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
-      s.base = __shfl_sync(0xffffffffu, mine.base, b & 31);
-      run = pa_own_run(a, s, sh.prefix);
-      tok0 = s.tok0;
-    };
-    if (b >= 0) load();
+  if (s0 < s1) {
+    Run run = prefix_run;
+    int tok0 = 0, i = 0, g = 0;
+    if (b >= 0) {
+      load(b >> 5);
+      run = own_run(b);
+      tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
+    }
     int items = run_items(run);
-    while (start < sh.s1) {
+    if (s0 > start) {
+      if (s0 - start >= head_cost) {
+        g = static_cast<int>(div_u64(s0 - start, head_cost));
+        start += g * head_cost;
+      }
+      i = pa_find_item(run, start, s0, &start);
+    }
+#pragma unroll 1
+    while (start < s1) {
       const int tokens = item_tokens(run, i);
       const int w = tokens > run.tpt ? 2 : 1;
       const int n = item_tiles(run, i, tokens);
-      share_tiles(start, w, n, sh.s0, sh.s1, &it.j0, &it.j1);
+      share_tiles(start, w, n, s0, s1, &it.j0, &it.j1);
       if (it.j0 < it.j1) {
         const int first = i * 2 * run.tpt;
         it.tok = tok0 + first;
@@ -470,12 +537,12 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
         it.head = b < 0 ? g : b * a.h_kv + g;
         it.end0 = w == 1 ? it.j1 : min(it.j1, max(it.j0, item_tiles(run, i, run.tpt)));
         it.pre_tiles = run.pre;
-        it.pre = sh.prefix;
+        it.pre = prefix;
         it.sees = run.base + first + 1;
         const bool whole = it.j0 == 0 && it.j1 == n;
-        it.flags = (w == 2 ? kPaTwo : 0) | (whole ? kPaWhole : 0) | (start < sh.s0 ? kPaCarried : 0) |
+        it.flags = (w == 2 ? kPaTwo : 0) | (whole ? kPaWhole : 0) | (start < s0 ? kPaCarried : 0) |
                    (it.j1 == n ? kPaEnds : 0) | (b < 0 ? kPaOnce : 0);
-        it.first_cta = whole ? blockIdx.x : share_owner(sh.total, sh.ctas, start);
+        it.first_cta = start < s0 ? share_owner(total, ctas, start) : blockIdx.x;
         if (!pass(it)) return;
       }
       start += cost_of(w, n);
@@ -485,9 +552,11 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
           g = 0;
           do {
             if (++b >= a.batch) break;
-            load();
+            load(b >> 5);
+            run = own_run(b);
           } while (run.n == 0);
           if (b >= a.batch) break;
+          tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
           items = run_items(run);
         }
       }
@@ -1191,8 +1260,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x)->valid = 0;
   tc_fence_before();
-  pa_find_share(a, sm);
+  __syncthreads();
   tc_fence_after();
+  if (a.batch > kPaWarpBatch) pa_find_share(a, sm);
   const uint32_t tmem = sm.tmem;
 
   // Registers: 512 x 128 at launch = 256 x 160 + 256 x 96, so that a thread of
@@ -1305,7 +1375,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
     start += cost_before(run, i);
     const int tokens = item_tokens(run, i), w = tokens > run.tpt ? 2 : 1, n = item_tiles(run, i, tokens);
     const int first = share_owner(meta.total, meta.ctas, start);
-    const int last = share_owner(meta.total, meta.ctas, start + static_cast<int64_t>(w) * (n - 1));
+    const int last = share_owner(meta.total, meta.ctas, start + static_cast<int64_t>(w == 2 ? kTileCost2 : kTileCost1) * (n - 1));
     if (first == last)
       s.add(reinterpret_cast<const float2*>(a.work + a.off_row_ml)[whole_row],
             reinterpret_cast<const float*>(a.work + a.off_row_o) + whole_row * kHeadDim + lane * 4, 0);

@@ -9,8 +9,7 @@
 //   a shared prefix taken once for all sequences: for g, for the runs of all packed tokens: its keys;
 //   the sequences: for b, for g, for the runs of b's tokens: the keys that the run's last token sees
 //   (behind those of the prefix where it is not taken for all together).
-// An item costs (row tiles) x (key tiles) + kItemCost; the costs of all items
-// laid end to end are cut into equal shares, one for each CTA, whatever the
+// The costs of all items (below) laid end to end are cut into equal shares, one for each CTA, whatever the
 // batch, the lengths and the heads.  A key tile belongs to the CTA in whose
 // share its place on that line falls, so a long item is split over CTAs.
 // Everything follows from the lengths in closed form (a sum of floors), so
@@ -21,8 +20,10 @@
 
 namespace qspec {
 
-constexpr int kItemCost = 2;       // an item's fixed cost (queries, output) in pairs of a row tile and a key tile
-constexpr int kMinShare = 6;       // a CTA's smallest share: fewer CTAs work where there is less
+// Costs, in units of about COSTUNIT cycles: a key tile for two row tiles or one, and what an item of
+// either kind costs besides (queries, first scores, output).
+constexpr int kTileCost2 = 4, kTileCost1 = 3, kItemCost2 = 8, kItemCost1 = 6;
+constexpr int kMinShare = 12;      // a CTA's smallest share: fewer CTAs work where there is less
 
 // Unsigned division; 64 bits only where they are needed (a 64-bit division is a long software routine).
 __host__ __device__ inline uint64_t div_u64(uint64_t a, uint64_t b) {
@@ -76,7 +77,8 @@ __host__ __device__ inline int item_tiles(const Run& r, int i, int tokens) {
 }
 
 __host__ __device__ inline int64_t cost_of(int row_tiles, int key_tiles) {
-  return (row_tiles == 2 ? 2ll * key_tiles : key_tiles) + kItemCost;
+  return row_tiles == 2 ? static_cast<int64_t>(kTileCost2) * key_tiles + kItemCost2
+                        : static_cast<int64_t>(kTileCost1) * key_tiles + kItemCost1;
 }
 
 // The cost of the items before item i (i <= run_items(r)).
@@ -91,7 +93,7 @@ __host__ __device__ inline int64_t cost_before(const Run& r, int i) {
   }
   const int64_t s = 2 * r.tpt;
   const int64_t own = r.base < 0 ? 0 : floor_sum_128(i, s, r.base + s + 127);
-  return 2 * (own + static_cast<int64_t>(i) * r.pre) + static_cast<int64_t>(i) * kItemCost + last;
+  return kTileCost2 * (own + static_cast<int64_t>(i) * r.pre) + static_cast<int64_t>(i) * kItemCost2 + last;
 }
 
 __host__ __device__ inline int64_t run_cost(const Run& r) {
@@ -104,22 +106,32 @@ __host__ __device__ inline int working_ctas(int64_t total, int grid) {
   const int most = static_cast<int>(total) / kMinShare;
   return most < 1 ? 1 : most;
 }
-__host__ __device__ inline int64_t share_start(int64_t total, int ctas, int c) {
-  return static_cast<int64_t>(div_u64(static_cast<uint64_t>(total) * c, ctas));
+// (equal but for one unit, the larger ones first: one division for both ends)
+__host__ __device__ inline void share_of(int64_t total, int ctas, int c, int64_t* s0, int64_t* s1) {
+  const int64_t each = static_cast<int64_t>(div_u64(total, ctas));
+  const int more = static_cast<int>(total - each * ctas);
+  *s0 = each * c + (c < more ? c : more);
+  *s1 = *s0 + each + (c < more ? 1 : 0);
 }
 __host__ __device__ inline int share_owner(int64_t total, int ctas, int64_t pos) {
-  return static_cast<int>(div_u64(static_cast<uint64_t>(pos + 1) * ctas - 1, total));
+  const int64_t each = static_cast<int64_t>(div_u64(total, ctas)), more = total - each * ctas;
+  const int64_t large = more * (each + 1);
+  return static_cast<int>(pos < large ? div_u64(pos, each + 1) : more + div_u64(pos - large, each));
 }
 
-// Key tiles [j0, j1) of an item at `start`, with w row tiles and n key tiles,
-// that fall into the share [s0, s1).
-__host__ __device__ inline void share_tiles(int64_t start, int w, int n, int64_t s0, int64_t s1, int* j0,
+// Key tiles [j0, j1) of an item at `start`, with n key tiles, that fall into the share [s0, s1).
+__host__ __device__ inline void share_tiles(int64_t start, int row_tiles, int n, int64_t s0, int64_t s1, int* j0,
                                             int* j1) {
-  const int up = w - 1;                                  // w is 1 or 2: a shift divides
-  const int64_t lo = s0 <= start ? 0 : (s0 - start + up) >> up;
-  const int64_t hi = s1 <= start ? 0 : (s1 - start + up) >> up;
-  *j0 = static_cast<int>(lo < n ? lo : n);
-  *j1 = static_cast<int>(hi < n ? hi : n);
+  const int64_t from = s0 <= start ? 0 : s0 - start, to = s1 <= start ? 0 : s1 - start;
+  const int64_t all = static_cast<int64_t>(n) * (row_tiles == 2 ? kTileCost2 : kTileCost1);
+  const uint64_t lo = from < all ? from : all, hi = to < all ? to : all;
+  if (row_tiles == 2) {
+    *j0 = static_cast<int>((lo + kTileCost2 - 1) / kTileCost2);
+    *j1 = static_cast<int>((hi + kTileCost2 - 1) / kTileCost2);
+  } else {
+    *j0 = static_cast<int>((lo + kTileCost1 - 1) / kTileCost1);
+    *j1 = static_cast<int>((hi + kTileCost1 - 1) / kTileCost1);
+  }
 }
 
 }  // namespace qspec

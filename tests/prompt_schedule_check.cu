@@ -63,7 +63,7 @@ int main() {
           e.n = item_tiles(r, i, tokens);
           if (e.n < 1) return fail("tiles", r.n, r.base, i);
           items.push_back(e);
-          pos += static_cast<int64_t>(e.w) * e.n + kItemCost;
+          pos += e.w == 2 ? kTileCost2 * e.n + kItemCost2 : kTileCost1 * e.n + kItemCost1;
         }
         if (run_cost(r) != pos - head) return fail("run_cost", r.n, r.base, g);
       }
@@ -94,11 +94,14 @@ int main() {
     for (int grid : grids) {
       const int ctas = working_ctas(total, grid);
       if (ctas < 1 || ctas > grid) return fail("ctas", total, grid, ctas);
-      if (share_start(total, ctas, 0) != 0 || share_start(total, ctas, ctas) != total) return fail("cover", total, ctas, 0);
+      int64_t reached = 0;
       std::vector<int> next(items.size(), 0), first(items.size(), -1), last(items.size(), -1);
       size_t from = 0;
       for (int c = 0; c < ctas; ++c) {
-        const int64_t s0 = share_start(total, ctas, c), s1 = share_start(total, ctas, c + 1);
+        int64_t s0, s1;
+        share_of(total, ctas, c, &s0, &s1);
+        if (s0 != reached || s1 <= s0) return fail("cover", total, ctas, c);
+        reached = s1;
         int begun = 0, carried = 0;
         while (from > 0 && items[from].start > s0) --from;
         while (from + 1 < items.size() && items[from + 1].start <= s0) ++from;
@@ -118,10 +121,11 @@ int main() {
         }
         if (begun > 1 || carried > 1) return fail("piece slots", c, begun, carried);
       }
+      if (reached != total) return fail("cover", total, ctas, reached);
       for (size_t i = 0; i < items.size(); ++i) {
         if (next[i] != items[i].n) return fail("tiles left", static_cast<long long>(i), next[i], items[i].n);
         if (share_owner(total, ctas, items[i].start) != first[i]) return fail("first", static_cast<long long>(i), first[i], ctas);
-        if (share_owner(total, ctas, items[i].start + static_cast<int64_t>(items[i].w) * (items[i].n - 1)) != last[i])
+        if (share_owner(total, ctas, items[i].start + static_cast<int64_t>(items[i].w == 2 ? kTileCost2 : kTileCost1) * (items[i].n - 1)) != last[i])
           return fail("last", static_cast<long long>(i), last[i], ctas);
       }
     }
