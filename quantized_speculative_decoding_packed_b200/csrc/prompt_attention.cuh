@@ -27,6 +27,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cstddef>
 #include <cstdint>
 
 #include "attention.cuh"
@@ -301,8 +302,9 @@ struct PaShare {
 };
 
 // Barriers and small exchanges in shared memory.
+constexpr int kPaBarriers = 2 * kPaStages + 17 + 2 * kPaItems;
 struct PaShared {
-  uint64_t kv_full[kPaStages], kv_empty[kPaStages], q_full[2], q_empty[2];
+  uint64_t kv_full[kPaStages], kv_empty[kPaStages], q_full[2], q_empty[2];      // (initialised in this order)
   uint64_t s_ready[2], p_ready[2], pv_done[2], o_free[2], ml_full[2], ml_free[2], drained;
   uint64_t item_full[kPaItems], item_empty[kPaItems];
   PaItem items[kPaItems];
@@ -1211,7 +1213,7 @@ __device__ __forceinline__ void pa_refuse(const PromptArgs& a) {
 __global__ void __launch_bounds__(kPaThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
-                            const __grid_constant__ CUtensorMap tm_pv, const PromptArgs a) {
+                            const __grid_constant__ CUtensorMap tm_pv, const __grid_constant__ PromptArgs a) {
   extern __shared__ __align__(1024) uint8_t pa_dyn[];
   PaShared& sm = *reinterpret_cast<PaShared*>(pa_dyn + kPaTilesBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1222,29 +1224,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   }
 
   if (warp == 8) {
-    if (lane == 0) {
-      for (int k = 0; k < kPaStages; ++k) {
-        mbar_init(smem_u32(&sm.kv_full[k]), 1);
-        mbar_init(smem_u32(&sm.kv_empty[k]), 1);
-      }
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(smem_u32(&sm.q_full[k]), 1);
-        mbar_init(smem_u32(&sm.q_empty[k]), 1);
-        mbar_init(smem_u32(&sm.s_ready[k]), 1);
-        mbar_init(smem_u32(&sm.p_ready[k]), 4);
-        mbar_init(smem_u32(&sm.pv_done[k]), 1);
-        mbar_init(smem_u32(&sm.o_free[k]), 4);
-        mbar_init(smem_u32(&sm.ml_full[k]), 4);
-        mbar_init(smem_u32(&sm.ml_free[k]), 4);
-      }
-      for (int k = 0; k < kPaItems; ++k) {
-        mbar_init(smem_u32(&sm.item_full[k]), 1);
-        mbar_init(smem_u32(&sm.item_empty[k]), 14);
-      }
-      mbar_init(smem_u32(&sm.drained), 1);
-      sm.abort_flag = 0;
-      fence_barrier_init();
-    }
+    // the barriers lie one after another: a lane initialises one, or two
+    auto count_of = [](int k) -> uint32_t {
+      constexpr int kQ = 2 * kPaStages;        // kv_full, kv_empty; q_full, q_empty, s_ready: one arrival
+      if (k < kQ + 6) return 1u;
+      if (k < kQ + 8) return 4u;               // p_ready
+      if (k < kQ + 10) return 1u;              // pv_done
+      if (k < kQ + 16) return 4u;              // o_free, ml_full, ml_free
+      if (k < kQ + 17 + kPaItems) return 1u;   // drained, item_full
+      return 14u;                              // item_empty: loads, products, 8 warps of softmax, 4 of output
+    };
+    static_assert(offsetof(PaShared, items) == 8 * kPaBarriers && kPaBarriers == 2 * kPaStages + 17 + 2 * kPaItems);
+    for (int k = lane; k < kPaBarriers; k += 32) mbar_init(smem_u32(&sm.kv_full[0]) + 8 * k, count_of(k));
+    if (lane == 0) sm.abort_flag = 0;
+    __syncwarp();
+    if (lane == 0) fence_barrier_init();
     if (lane == 1) prefetch_tensormap(&tm_q);
     if (lane == 2) prefetch_tensormap(&tm_k);
     if (lane == 3) prefetch_tensormap(&tm_v);

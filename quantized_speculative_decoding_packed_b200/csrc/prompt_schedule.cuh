@@ -31,13 +31,23 @@ __host__ __device__ inline uint64_t div_u64(uint64_t a, uint64_t b) {
   return a / b;
 }
 
-// sum over i < n of floor((a i + b) / 128), for n, b < 2^31 and a <= 256: Euclid's steps on
-// (a, 128).  After the first, which only shifts, every term but n is below 128.
-__host__ __device__ inline int64_t floor_sum_128(int64_t n, int64_t a, int64_t b) {
+// sum over i < n of floor((s i + b) / 128), for n, b < 2^31 and 0 < s <= 256.
+// Where s is a power of two (so are most groups of heads), shifts alone:
+// below 128, floor((s i + b) / 128) = floor((i + floor(b / s)) / (128 / s)).
+// Else Euclid's steps on (s, 128); after the first every term but n is below 128.
+__host__ __device__ inline int64_t floor_sum_128(int64_t n, int s, int64_t b) {
   if (n <= 0) return 0;
-  int64_t ans = (n - 1) * n / 2 * (a >> 7) + n * (b >> 7);
-  a &= 127;
-  uint64_t y = static_cast<uint64_t>(a) * n + (b & 127);
+  if ((s & (s - 1)) == 0) {
+    if (s >= 128) return n * (b >> 7) + (s >> 7) * (n * (n - 1) / 2);
+    int k = 0;                                           // 128 / s = 2^k
+    while ((s << k) < 128) ++k;
+    const int64_t e = b >> (7 - k), last = n + e;
+    const int64_t q0 = e >> k, r0 = e - (q0 << k), q1 = last >> k, r1 = last - (q1 << k);
+    return ((q1 * (q1 - 1) / 2) << k) + q1 * r1 - ((q0 * (q0 - 1) / 2) << k) - q0 * r0;
+  }
+  int64_t ans = (n - 1) * n / 2 * (s >> 7) + n * (b >> 7);
+  const uint64_t a = s & 127;
+  uint64_t y = a * n + (b & 127);
   if (y < 128) return ans;
   uint64_t m = a, k = y >> 7, c = y & 127, d = 128;     // sum over i < k of floor((d i + c) / m)
   for (;;) {
@@ -64,7 +74,9 @@ struct Run {
   int pre;         // key tiles that every token sees
 };
 
-__host__ __device__ inline int run_items(const Run& r) { return (r.n + 2 * r.tpt - 1) / (2 * r.tpt); }
+__host__ __device__ inline int run_items(const Run& r) {
+  return r.n <= 2 * r.tpt ? (r.n > 0 ? 1 : 0) : (r.n + 2 * r.tpt - 1) / (2 * r.tpt);
+}
 
 __host__ __device__ inline int item_tokens(const Run& r, int i) {
   const int left = r.n - i * 2 * r.tpt;
@@ -91,8 +103,8 @@ __host__ __device__ inline int64_t cost_before(const Run& r, int i) {
       last = cost_of(tokens > r.tpt ? 2 : 1, item_tiles(r, i, tokens));
     }
   }
-  const int64_t s = 2 * r.tpt;
-  const int64_t own = r.base < 0 ? 0 : floor_sum_128(i, s, r.base + s + 127);
+  const int s = 2 * r.tpt;
+  const int64_t own = r.base < 0 || i == 0 ? 0 : floor_sum_128(i, s, static_cast<int64_t>(r.base) + s + 127);
   return kTileCost2 * (own + static_cast<int64_t>(i) * r.pre) + static_cast<int64_t>(i) * kItemCost2 + last;
 }
 

@@ -34,7 +34,8 @@ static unsigned rnd(unsigned n) {
 
 int main() {
   for (int k = 0; k < 40000; ++k) {
-    const int64_t n = rnd(k & 1 ? 200 : 20000), a = 1 + rnd(256), b = rnd(k & 2 ? 100000 : 2000000000);
+    const int64_t n = rnd(k & 1 ? 200 : 20000), b = rnd(k & 2 ? 100000 : 2000000000);
+    const int a = k % 3 ? 1 + rnd(256) : 1 << rnd(9);
     int64_t want = 0;
     for (int64_t i = 0; i < n; ++i) want += (a * i + b) / 128;
     if (floor_sum_128(n, a, b) != want) return fail("floor_sum_128", n, a, b);

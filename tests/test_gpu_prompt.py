@@ -145,6 +145,17 @@ def test_prefill_strides_and_padding_rows(qs):
     assert bool((wide[:, h_q * D:] == 7).all()) and bool((wide[sum(new):] == 7).all())
 
 
+@pytest.mark.parametrize("new,old,h_q,h_kv", [([300, 1, 2000], [1000, 4000, 0], 4, 2), ([1500], [9000], 8, 1),
+                                              ([3], [40000], 2, 1)])
+def test_prefill_is_the_same_every_time(qs, new, old, h_q, h_kv):
+    """Pieces of split items are joined in their order, whichever CTA comes last."""
+    q, kc, vc, cu, lens = _case(12, new, old, h_q, h_kv)
+    want = qs.attn_prefill(q, cu, lens, kc, vc, h_q)
+    _check(want, new, old, q, kc, vc, h_q)
+    for _ in range(20):
+        assert torch.equal(qs.attn_prefill(q, cu, lens, kc, vc, h_q), want)
+
+
 def test_prefill_extreme_scores(qs):
     """Scores that rise along the keys (the running maximum moves in every tile), fall, and are all equal."""
     h_q = h_kv = 3
