@@ -55,7 +55,7 @@ struct PromptArgs {
   uint16_t* out;
   uint8_t* work;
   int64_t ld_out;
-  int64_t off_start, off_desc, off_ml, off_o, off_row_ml, off_row_o;
+  int64_t off_owners, off_desc, off_ml, off_o, off_row_ml, off_row_o;
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
 };
 
@@ -64,27 +64,22 @@ struct PaJoin {
   int32_t valid, first, tok, tokens, g, pad[3];
 };
 
-struct PaMeta {
-  int64_t total;
-  int32_t ctas;
-  int32_t prefix;              // the prefix's length, -1 where it is refused
-};
-
 // Workspace: status word, what the GEMMs keep there, then per CTA two pieces of two row tiles
-// (O in blocks of 4 columns: [32][128 rows][4]); with a prefix taken once, for each (token, head)
-// a row for its prefix and one for its own keys.
-constexpr int64_t kPaOffMeta = 8192;
+// (O in blocks of 4 columns: [32][128 rows][4]); with a prefix taken once, for the prefix and for own
+// keys, by an item's first token and KV head, the CTAs that have its pieces (first, last), and for each
+// (token, head) a whole row.
+constexpr int64_t kPaOffDesc = 8192;
 struct PaLayout {
-  int64_t off_start, off_desc, off_ml, off_o, off_row_ml, off_row_o, total;
+  int64_t off_owners, off_desc, off_ml, off_o, off_row_ml, off_row_o, total;
 };
-__host__ __device__ inline PaLayout pa_layout(int64_t grid, int64_t batch, int64_t rows, bool prefix) {
+__host__ __device__ inline PaLayout pa_layout(int64_t grid, int64_t kv_rows, int64_t rows, bool prefix) {
   PaLayout l;
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-  l.off_desc = kPaOffMeta + 256;
+  l.off_desc = kPaOffDesc;
   l.off_ml = up(l.off_desc + grid * static_cast<int64_t>(sizeof(PaJoin)));
   l.off_o = up(l.off_ml + grid * 4 * 128 * 8);
-  l.off_start = up(l.off_o + grid * 4 * 128 * kHeadDim * 4);
-  l.off_row_ml = up(l.off_start + (prefix ? batch * 8 : 0));
+  l.off_owners = up(l.off_o + grid * 4 * 128 * kHeadDim * 4);
+  l.off_row_ml = up(l.off_owners + (prefix ? 2 * kv_rows * 8 : 0));
   l.off_row_o = up(l.off_row_ml + (prefix ? 2 * rows * 8 : 0));
   l.total = l.off_row_o + (prefix ? 2 * rows * kHeadDim * 4 : 0);
   return l;
@@ -394,14 +389,12 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
     sm.share.start = 0;
   }
   __syncthreads();
-  int64_t* const starts = a.mode == kPaPrefixOnce ? reinterpret_cast<int64_t*>(a.work + a.off_start) : nullptr;
   before = prefix_all;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
     const int b = b0 + tid;
     if (a.batch > kPaThreads) scan(b);           // else this thread's values still stand
     if (b < a.batch) {
-      if (c == 0 && starts) starts[b] = at;
       if (cost > 0 && at <= s0 && s0 < at + cost * a.h_kv) {
         sm.share.b = b;
         sm.share.start = at;
@@ -473,11 +466,6 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
       start = __shfl_sync(0xffffffffu, in0 ? at[0] : at[1], of);
       head_cost = __shfl_sync(0xffffffffu, in0 ? cost[0] : cost[1], of);
     }
-    if (blockIdx.x == 0 && a.mode == kPaPrefixOnce) {
-      int64_t* const starts = reinterpret_cast<int64_t*>(a.work + a.off_start);
-      if (lane < a.batch) starts[lane] = at[0];
-      if (lane + 32 < a.batch) starts[lane + 32] = at[1];
-    }
   } else {
     total = sm.share.total;
     ctas = sm.share.ctas;
@@ -490,12 +478,24 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
       head_cost = pa_run_cost(own_run(b));
     }
   }
-  if (blockIdx.x == 0 && lane == 0) {
-    PaMeta* meta = reinterpret_cast<PaMeta*>(a.work + kPaOffMeta);
-    meta->total = total;
-    meta->ctas = ctas;
-    meta->prefix = prefix;
+  PaItem it;
+  Run run = prefix_run;
+  int tok0 = 0, i = 0, g = 0;
+  if (s0 < s1) {
+    if (b >= 0) {
+      load(b >> 5);
+      run = own_run(b);
+      tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
+    }
+    if (s0 > start) {
+      if (s0 - start >= head_cost) {
+        g = static_cast<int>(div_u64(s0 - start, head_cost));
+        start += g * head_cost;
+      }
+      i = pa_find_item(run, start, s0, &start);
+    }
   }
+  if (a.batch <= kPaWarpBatch) __syncthreads();   // the barriers are there (the other warps have waited for this one)
   uint32_t count = 0;
   auto pass = [&](const PaItem& it) -> bool {
     const uint32_t slot = count % kPaItems;
@@ -508,23 +508,8 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
     ++count;
     return true;
   };
-  PaItem it;
   if (s0 < s1) {
-    Run run = prefix_run;
-    int tok0 = 0, i = 0, g = 0;
-    if (b >= 0) {
-      load(b >> 5);
-      run = own_run(b);
-      tok0 = __shfl_sync(0xffffffffu, mine.tok0, b & 31);
-    }
     int items = run_items(run);
-    if (s0 > start) {
-      if (s0 - start >= head_cost) {
-        g = static_cast<int>(div_u64(s0 - start, head_cost));
-        start += g * head_cost;
-      }
-      i = pa_find_item(run, start, s0, &start);
-    }
 #pragma unroll 1
     while (start < s1) {
       const int tokens = item_tokens(run, i);
@@ -545,6 +530,12 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
         it.flags = (w == 2 ? kPaTwo : 0) | (whole ? kPaWhole : 0) | (start < s0 ? kPaCarried : 0) |
                    (it.j1 == n ? kPaEnds : 0) | (b < 0 ? kPaOnce : 0);
         it.first_cta = start < s0 ? share_owner(total, ctas, start) : blockIdx.x;
+        if (a.mode == kPaPrefixOnce && it.j0 == 0) {
+          const int64_t end = start + static_cast<int64_t>(w == 2 ? kTileCost2 : kTileCost1) * (n - 1);
+          const int last = whole ? blockIdx.x : share_owner(total, ctas, end);
+          const int64_t at = (b < 0 ? 0 : static_cast<int64_t>(a.n_tok) * a.h_kv) + static_cast<int64_t>(it.tok) * a.h_kv + g;
+          if (lane == 0) reinterpret_cast<int2*>(a.work + a.off_owners)[at] = make_int2(blockIdx.x, last);
+        }
         if (!pass(it)) return;
       }
       start += cost_of(w, n);
@@ -1254,9 +1245,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x)->valid = 0;
   tc_fence_before();
-  __syncthreads();
+  if (a.batch > kPaWarpBatch) {
+    __syncthreads();
+    pa_find_share(a, sm);
+  } else if (warp != 10) {
+    __syncthreads();                     // warp 10 comes to it when it has its first item
+  }
   tc_fence_after();
-  if (a.batch > kPaWarpBatch) pa_find_share(a, sm);
   const uint32_t tmem = sm.tmem;
 
   // Registers: 512 x 128 at launch = 256 x 160 + 256 x 96, so that a thread of
@@ -1281,77 +1276,89 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining pieces
-// A row's pieces (m, l, O) in order: out = sum e^(m_p - M) O_p / sum e^(m_p - M) l_p.
-// A thread holds kCols of its columns.
-template <int kQuads>
-struct PaJoined {
-  float m = -INFINITY, l = 0.f;
-  float4 o[kQuads];
-  __device__ __forceinline__ PaJoined() {
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  // the columns src + k * stride
-  __device__ __forceinline__ void add(float2 ml, const float* src, int64_t stride) {
-    if (ml.x == -INFINITY || ml.y <= 0.f) return;          // nothing seen: O is not read
-    const float top = fmaxf(m, ml.x);
-    const float f = m == -INFINITY ? 0.f : ex2((m - top) * kScoreLog2);
-    const float g = ex2((ml.x - top) * kScoreLog2);
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(src + k * stride);
-      o[k].x = o[k].x * f + v.x * g;
-      o[k].y = o[k].y * f + v.y * g;
-      o[k].z = o[k].z * f + v.z * g;
-      o[k].w = o[k].w * f + v.w * g;
-    }
-    l = l * f + ml.y * g;
-    m = top;
-  }
-  // pieces of CTAs first .. last of row tile x, from block `quad` of 4 columns on
-  __device__ __forceinline__ void pieces(const PromptArgs& a, int first, int last, int x, int row, int quad) {
-    for (int c = first; c <= last; ++c) {
-      const int64_t tile = (static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + x;
-      add(reinterpret_cast<const float2*>(a.work + a.off_ml)[tile * 128 + row],
-          reinterpret_cast<const float*>(a.work + a.off_o) + tile * 128 * kHeadDim + (quad * 128 + row) * 4, 128 * 4);
-    }
-  }
-  __device__ __forceinline__ void store(const PromptArgs& a, int64_t tok, int head, int quad) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* const dst = a.out + tok * a.ld_out + static_cast<int64_t>(head) * kHeadDim + quad * 4;
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k)
-      *reinterpret_cast<uint2*>(dst + k * 4) =
-          make_uint2(cvt_bf16x2(o[k].x * inv, o[k].y * inv), cvt_bf16x2(o[k].z * inv, o[k].w * inv));
-  }
-};
+// A row's pieces (m, l, O) in order: out = sum e^(m_p - M) O_p / sum e^(m_p - M) l_p.  Bound by the
+// latency of L2: all maxima of a row are loaded at once, then all of its O.
+__device__ __forceinline__ int64_t pa_piece_tile(int cta, int first, int x) {
+  return (static_cast<int64_t>(cta) * 2 + (cta == first ? 1 : 0)) * 2 + x;
+}
+// The weight of a piece under the maximum of all; 0 for one that has seen nothing (its O is not taken).
+__device__ __forceinline__ float pa_piece_weight(float m, float top) {
+  return m == -INFINITY ? 0.f : ex2((m - top) * kScoreLog2);
+}
 
-// Split items of packed prompts: grid (CTAs of the attention, 8), 8 warps.  A block takes 32 rows, a
-// lane for each (as they lie in the pieces), a warp 16 columns.
+// Split items: grid (CTAs of the attention, 8), 8 warps.  A block takes 32 rows, a lane for each (as they
+// lie in the pieces), a warp 16 columns.
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const PaJoin j = reinterpret_cast<const PaJoin*>(a.work + a.off_desc)[blockIdx.x];
   if (!j.valid) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int x = blockIdx.y >> 2;
+  const int x = blockIdx.y >> 2, last = blockIdx.x;
   const int row = (blockIdx.y & 3) * 32 + lane;
   const int t = row / a.group;
   if (t >= a.tpt || x * a.tpt + t >= j.tokens) return;
-  PaJoined<4> s;
-  s.pieces(a, j.first, blockIdx.x, x, row, warp * 4);
-  s.store(a, j.tok + x * a.tpt + t, j.g * a.group + row - t * a.group, warp * 4);
+  const float2* const ml = reinterpret_cast<const float2*>(a.work + a.off_ml) + row;
+  const float* const o = reinterpret_cast<const float*>(a.work + a.off_o) + (warp * 4 * 128 + row) * 4;
+  float m = -INFINITY, l = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int p = j.first; p <= last; p += 2) {       // almost always there are two
+    float2 s[2];
+    float4 v[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t tile = pa_piece_tile(min(p + e, last), j.first, x);
+      s[e] = ml[tile * 128];
+      if (p + e > last) s[e] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[e][k] = *reinterpret_cast<const float4*>(o + tile * 128 * kHeadDim + k * 128 * 4);
+    }
+    const float top = max3(m, s[0].x, s[1].x);
+    const float f = pa_piece_weight(m, top);
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float w = pa_piece_weight(s[e].x, top);
+      l = fmaf(s[e].y, w, l);
+      if (w > 0.f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[k].x = fmaf(v[e][k].x, w, acc[k].x);
+          acc[k].y = fmaf(v[e][k].y, w, acc[k].y);
+          acc[k].z = fmaf(v[e][k].z, w, acc[k].z);
+          acc[k].w = fmaf(v[e][k].w, w, acc[k].w);
+        }
+      }
+    }
+    m = top;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* const dst = a.out + static_cast<int64_t>(j.tok + x * a.tpt + t) * a.ld_out +
+                        static_cast<int64_t>(j.g * a.group + row - t * a.group) * kHeadDim + warp * 16;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2)
+    *reinterpret_cast<uint4*>(dst + k * 4) =
+        make_uint4(cvt_bf16x2(acc[k].x * inv, acc[k].y * inv), cvt_bf16x2(acc[k].z * inv, acc[k].w * inv),
+                   cvt_bf16x2(acc[k + 1].x * inv, acc[k + 1].y * inv), cvt_bf16x2(acc[k + 1].z * inv, acc[k + 1].w * inv));
 }
 
-// Every row behind a prefix taken once: its prefix's pieces, then its own keys'.  A warp a row.
+// Every row behind a prefix taken once: its prefix's pieces, then its own keys'.  A warp a row: a lane
+// looks after one piece (of 32), then after four columns.
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (r >= static_cast<int64_t>(a.n_tok) * a.h_q) return;
-  const int tok = static_cast<int>(r / a.h_q), head = static_cast<int>(r - static_cast<int64_t>(tok) * a.h_q);
+  const int64_t rows = static_cast<int64_t>(a.n_tok) * a.h_q;
+  if (r >= rows) return;
+  const int tok = static_cast<int>(div_u64(r, a.h_q)), head = static_cast<int>(r - static_cast<int64_t>(tok) * a.h_q);
   const int g = head / a.group;
+  const int prefix = pa_prefix(a);
   int b;
   if (a.cu) {
     if (tok >= a.cu[a.batch] || tok < a.cu[0]) return;
@@ -1361,29 +1368,74 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   }
   const PaSequence seq = pa_sequence(a, b);
   const int t = tok - seq.tok0;
-  const PaMeta meta = *reinterpret_cast<const PaMeta*>(a.work + kPaOffMeta);
-  if (seq.bad || t < 0 || t >= seq.n || meta.prefix < 0) return;   // what is refused is zero already
-  PaJoined<1> s;
-  auto part = [&](const Run& run, int64_t start, int t, int64_t whole_row) {   // t: the token's place in the run
-    const int i = t / (2 * a.tpt), x = (t / a.tpt) & 1;
-    start += cost_before(run, i);
-    const int tokens = item_tokens(run, i), w = tokens > run.tpt ? 2 : 1, n = item_tiles(run, i, tokens);
-    const int first = share_owner(meta.total, meta.ctas, start);
-    const int last = share_owner(meta.total, meta.ctas, start + static_cast<int64_t>(w == 2 ? kTileCost2 : kTileCost1) * (n - 1));
-    if (first == last)
-      s.add(reinterpret_cast<const float2*>(a.work + a.off_row_ml)[whole_row],
-            reinterpret_cast<const float*>(a.work + a.off_row_o) + whole_row * kHeadDim + lane * 4, 0);
-    else
-      s.pieces(a, first, last, x, (t % a.tpt) * a.group + head - g * a.group, lane);
-  };
-  if (meta.prefix > 0) {
-    const Run run = pa_prefix_run(a, meta.prefix);
-    part(run, run_cost(run) * g, tok, r);
+  if (seq.bad || t < 0 || t >= seq.n || prefix < 0) return;        // what is refused is zero already
+  // the CTAs that have the pieces of the prefix's item, and of the own one
+  const int2* const owners = reinterpret_cast<const int2*>(a.work + a.off_owners);
+  const int in0 = tok % (2 * a.tpt), in1 = t < 2 * a.tpt ? t : t % (2 * a.tpt);     // the token's place in its item
+  const int2 c0 = prefix > 0 ? owners[static_cast<int64_t>(tok - in0) * a.h_kv + g] : make_int2(0, -1);
+  const int2 c1 = owners[static_cast<int64_t>(a.n_tok) * a.h_kv + static_cast<int64_t>(tok - in1) * a.h_kv + g];
+  const int n0 = c0.y - c0.x + 1, n = n0 + c1.y - c1.x + 1;
+  const int in_group = head - g * a.group;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int p0 = 0; p0 < n; p0 += 32) {
+    float2 s = make_float2(-INFINITY, 0.f);
+    int64_t at = 0;                                    // where its O is, in 4 floats; whole rows: ~(where)
+    if (p0 + lane < n) {
+      const bool own = p0 + lane >= n0;
+      const int2 c = own ? c1 : c0;
+      if (c.x == c.y) {
+        const int64_t row = own ? rows + r : r;
+        s = reinterpret_cast<const float2*>(a.work + a.off_row_ml)[row];
+        at = ~(row * 32);
+      } else {
+        const int in = own ? in1 : in0, x = in >= a.tpt ? 1 : 0, row = (in - x * a.tpt) * a.group + in_group;
+        const int64_t tile = pa_piece_tile(c.x + p0 + lane - (own ? n0 : 0), c.x, x);
+        s = reinterpret_cast<const float2*>(a.work + a.off_ml)[tile * 128 + row];
+        at = tile * 4096 + row;
+      }
+    }
+    float top = fmaxf(m, s.x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float f = pa_piece_weight(m, top);
+    const float w = pa_piece_weight(s.x, top);
+    float sum = s.y * w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    l = l * f + sum;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    m = top;
+    const int here = min(32, n - p0);
+#pragma unroll 1
+    for (int q0 = 0; q0 < here; q0 += 4) {
+      float4 v[4];
+      float wq[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int q = min(q0 + e, here - 1);
+        wq[e] = __shfl_sync(0xffffffffu, w, q);
+        if (q0 + e >= here) wq[e] = 0.f;
+        const int64_t qa = __shfl_sync(0xffffffffu, at, q);
+        const float4* src = qa < 0 ? reinterpret_cast<const float4*>(a.work + a.off_row_o) + ~qa + lane
+                                   : reinterpret_cast<const float4*>(a.work + a.off_o) + qa + lane * 128;
+        v[e] = *src;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (wq[e] > 0.f) {
+          acc.x = fmaf(v[e].x, wq[e], acc.x);
+          acc.y = fmaf(v[e].y, wq[e], acc.y);
+          acc.z = fmaf(v[e].z, wq[e], acc.z);
+          acc.w = fmaf(v[e].w, wq[e], acc.w);
+        }
+      }
+    }
   }
-  const Run run = pa_own_run(a, seq, meta.prefix);
-  part(run, reinterpret_cast<const int64_t*>(a.work + a.off_start)[b] + run_cost(run) * g, t,
-       static_cast<int64_t>(a.n_tok) * a.h_q + r);
-  s.store(a, tok, head, lane);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(tok) * a.ld_out + static_cast<int64_t>(head) * kHeadDim + lane * 4) =
+      make_uint2(cvt_bf16x2(acc.x * inv, acc.y * inv), cvt_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace qspec

@@ -457,7 +457,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   qspec_status st = current_device(&dev, &info);
   if (st != QSPEC_OK) return st;
   const int grid = info.sm_count;
-  const PaLayout lay = pa_layout(grid, batch, n_tok * h_q, with_prefix);
+  const PaLayout lay = pa_layout(grid, n_tok * h_q, n_tok * h_q, with_prefix);
   if (workspace_bytes < static_cast<size_t>(lay.total)) return QSPEC_ERR_WORKSPACE_TOO_SMALL;
   static std::atomic<bool> attr_set[kMaxDevices];
   if (!attr_set[dev].load(std::memory_order_acquire)) {
@@ -475,7 +475,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.out = out;
   a.work = static_cast<uint8_t*>(workspace);
   a.ld_out = ld_out;
-  a.off_start = lay.off_start;
+  a.off_owners = lay.off_owners;
   a.off_desc = lay.off_desc;
   a.off_ml = lay.off_ml;
   a.off_o = lay.off_o;
@@ -878,7 +878,7 @@ size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t
     return 0;
   DeviceInfo info;
   if (current_device(nullptr, &info) != QSPEC_OK) return 0;
-  return static_cast<size_t>(pa_layout(info.sm_count, batch, n_tokens * h_q, true).total);
+  return static_cast<size_t>(pa_layout(info.sm_count, n_tokens * h_q, n_tokens * h_q, true).total);
 }
 
 qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
