@@ -57,6 +57,7 @@ struct PromptArgs {
   int64_t ld_out;
   int64_t off_owners, off_desc, off_ml, off_o, off_row_ml, off_row_o;
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
+  int parts;                   // > 0: few items, each has so many CTAs of its own (grid: parts x items)
 };
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
@@ -290,6 +291,9 @@ struct PaItem {
 };
 enum : int { kPaTwo = 1, kPaWhole = 2, kPaCarried = 4, kPaEnds = 8, kPaOnce = 16 };
 
+// The CTA's number.
+__device__ __forceinline__ int pa_cta() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 struct PaShare {
   int64_t s0, s1, total;
   int64_t start;               // of the sequence in which the share begins
@@ -405,10 +409,86 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
 }
 
 // ---------------------------------------------------------------- the roles of the warps
+// Few items (at most 32 sequences): item blockIdx.y of them in their order, or one of its parts; false
+// where there are not so many.  A part has four key tiles at least.
+__device__ __forceinline__ bool pa_find_one(const PromptArgs& a, PaItem* it) {
+  const int lane = threadIdx.x & 31;
+  const int prefix = pa_prefix(a);
+  PaSequence mine;
+  mine.n = 0;
+  if (lane < a.batch) mine = pa_sequence(a, lane);
+  Run run = pa_prefix_run(a, prefix);
+  int k = blockIdx.y, b = -1, tok0 = 0, items = run_items(run);
+  if (k >= items * a.h_kv) {
+    k -= items * a.h_kv;
+    const Run own = pa_own_run(a, mine, prefix);
+    const int each = run_items(own), all = each * a.h_kv;
+    int incl = all;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const uint32_t after = __ballot_sync(0xffffffffu, k < incl);
+    if (after == 0) return false;
+    b = __ffs(after) - 1;
+    k -= __shfl_sync(0xffffffffu, incl - all, b);
+    items = __shfl_sync(0xffffffffu, each, b);
+    run.n = __shfl_sync(0xffffffffu, own.n, b);
+    run.base = __shfl_sync(0xffffffffu, own.base, b);
+    run.pre = own.pre;
+    tok0 = __shfl_sync(0xffffffffu, mine.tok0, b);
+  }
+  const int g = items == 1 ? k : k / items, i = items == 1 ? 0 : k - g * items;
+  const int tokens = item_tokens(run, i), n = item_tiles(run, i, tokens), w = tokens > run.tpt ? 2 : 1;
+  const int parts = min(a.parts, (n + 3) >> 2), part = blockIdx.x;
+  if (part >= parts) return false;
+  const int first = i * 2 * run.tpt;
+  it->tok = tok0 + first;
+  it->tokens = tokens;
+  it->g = g;
+  it->head = b < 0 ? g : b * a.h_kv + g;
+  it->j0 = parts == 1 ? 0 : static_cast<int>(static_cast<int64_t>(n) * part / parts);
+  it->j1 = parts == 1 ? n : static_cast<int>(static_cast<int64_t>(n) * (part + 1) / parts);
+  it->end0 = w == 1 ? it->j1 : min(it->j1, max(it->j0, item_tiles(run, i, run.tpt)));
+  it->pre_tiles = run.pre;
+  it->pre = prefix;
+  it->sees = run.base + first + 1;
+  it->flags = (w == 2 ? kPaTwo : 0) | (parts == 1 ? kPaWhole : 0) | (part > 0 ? kPaCarried : 0) |
+              (part == parts - 1 ? kPaEnds : 0) | (b < 0 ? kPaOnce : 0);
+  it->first_cta = pa_cta() - part;
+  if (a.mode == kPaPrefixOnce && part == 0 && lane == 0) {
+    const int64_t at = (b < 0 ? 0 : static_cast<int64_t>(a.n_tok) * a.h_kv) + static_cast<int64_t>(it->tok) * a.h_kv + g;
+    reinterpret_cast<int2*>(a.work + a.off_owners)[at] = make_int2(it->first_cta, it->first_cta + parts - 1);
+  }
+  return true;
+}
+
+// Passes an item on (its number `count` in the CTA).
+__device__ __forceinline__ bool pa_pass(PaShared& sm, const PaItem& it, uint32_t count, uint32_t* status) {
+  const uint32_t slot = count % kPaItems;
+  if (!pa_wait(smem_u32(&sm.item_empty[slot]), ((count / kPaItems) & 1) ^ 1, &sm.abort_flag, status)) return false;
+  if ((threadIdx.x & 31) == 0) {
+    sm.items[slot] = it;
+    mbar_arrive(smem_u32(&sm.item_full[slot]));
+  }
+  __syncwarp();
+  return true;
+}
+
 // Warp 10: the share's items in order, into the ring.
 __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm) {
   const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
+  if (a.parts > 0) {
+    PaItem one;
+    const bool there = pa_find_one(a, &one);
+    __syncthreads();             // the barriers are there (the other warps have waited for this one)
+    if (there) pa_pass(sm, one, 0, status);
+    one.tokens = 0;
+    pa_pass(sm, one, there ? 1 : 0, status);
+    return;
+  }
   const int prefix = pa_prefix(a);
   const Run prefix_run = pa_prefix_run(a, prefix);
   const int64_t prefix_head = pa_run_cost(prefix_run);
@@ -497,17 +577,6 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
   }
   if (a.batch <= kPaWarpBatch) __syncthreads();   // the barriers are there (the other warps have waited for this one)
   uint32_t count = 0;
-  auto pass = [&](const PaItem& it) -> bool {
-    const uint32_t slot = count % kPaItems;
-    if (!pa_wait(smem_u32(&sm.item_empty[slot]), ((count / kPaItems) & 1) ^ 1, &sm.abort_flag, status)) return false;
-    if (lane == 0) {
-      sm.items[slot] = it;
-      mbar_arrive(smem_u32(&sm.item_full[slot]));
-    }
-    __syncwarp();
-    ++count;
-    return true;
-  };
   if (s0 < s1) {
     int items = run_items(run);
 #pragma unroll 1
@@ -536,7 +605,7 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
           const int64_t at = (b < 0 ? 0 : static_cast<int64_t>(a.n_tok) * a.h_kv) + static_cast<int64_t>(it.tok) * a.h_kv + g;
           if (lane == 0) reinterpret_cast<int2*>(a.work + a.off_owners)[at] = make_int2(blockIdx.x, last);
         }
-        if (!pass(it)) return;
+        if (!pa_pass(sm, it, count++, status)) return;
       }
       start += cost_of(w, n);
       if (++i >= items) {
@@ -556,7 +625,7 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
     }
   }
   it.tokens = 0;
-  pass(it);
+  pa_pass(sm, it, count, status);
 }
 
 // Waits for item `count` of the ring; its readers say when they have it.
@@ -643,62 +712,75 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
   int j0 = 0, j1 = 0, end0 = 0, pre_tiles = 0, pre = 0, last_sees = 0;
   bool two = false, has0 = false;
   uint32_t count = 0;                        // items taken
-  uint32_t ring = 0, qn = 0, singles = 0;    // key tiles x 2, query tiles, steps of items with one row tile
-  // the next S: its slot, whether its queries and keys are not known to have landed
+  uint32_t qn = 0, singles = 0;              // query tiles, steps of items with one row tile
+  // the ring place of the next S's keys (its values are in the next place), and the phase of its barrier
+  uint32_t k_st = 0, k_ph = 0;
+  auto forth = [](uint32_t& st, uint32_t& ph, uint32_t by) {
+    st += by;
+    if (st >= kPaStages) {
+      st -= kPaStages;
+      ph ^= 1;
+    }
+  };
+  // the next S: its slot and queries, whether these and the keys are not known to have landed
   int j = 0;
   uint32_t slot = 0, q = 0;
-  bool have_s = false, new_q = false, new_k = false;
-  // P V to come, in order: ring place of the values, tail | flags
-  uint32_t pv_r[2] = {0, 0}, pv_w[2] = {0, 0}, ahead = 0, busy = 0;
-  constexpr uint32_t kSlot = 256, kFirst = 512, kFree = 1024, kLast = 2048, kNew = 4096;
+  bool new_q = false, new_k = false;
+  // P V to come of either slot: tail, ring place, phase, flags; which comes first
+  constexpr uint32_t kStage = 256, kPhase = 2048, kFirst = 4096, kFree = 8192, kLast = 16384, kNew = 32768, kHave = 65536;
+  uint32_t e0 = 0, e1 = 0, oldest = 0;
   uint32_t p_count = 0;                      // phases of p_ready: slot 0 in bit 0, slot 1 in bit 1
-  uint32_t o_count[2] = {0, 0};              // items with steps in the slots
+  uint32_t o_count0 = 0, o_count1 = 0;       // items with steps in the slots
+  auto tail_of = [&](int t) -> int {         // keys seen of tile t and those after it
+    return t < pre_tiles ? pre - t * 128 : last_sees - (t - pre_tiles) * 128;
+  };
+  const uint32_t kv_full = smem_u32(&sm.kv_full[0]), kv_empty = smem_u32(&sm.kv_empty[0]);
   while (ok) {
-    if (!have_s && more) {
-      if (!in_item) {
-        const uint32_t bar = smem_u32(&sm.item_full[count % kPaItems]), ph = (count / kPaItems) & 1;
-        bool got = __all_sync(0xffffffffu, mbar_test_wait(bar, ph));
-        if (!got && ahead == 0) {
-          ok = got = pa_wait(bar, ph, abort_flag, status);
+    if (!in_item && more) {
+      const uint32_t bar = smem_u32(&sm.item_full[count % kPaItems]), ph = (count / kPaItems) & 1;
+      bool got = __all_sync(0xffffffffu, mbar_test_wait(bar, ph));
+      if (!got && !((e0 | e1) & kHave)) {
+        ok = got = pa_wait(bar, ph, abort_flag, status);
+        if (!ok) break;
+      }
+      if (got) {
+        const int mine = lane < 12 ? reinterpret_cast<const int32_t*>(&sm.items[count % kPaItems])[lane] : 0;
+        const int tokens = __shfl_sync(0xffffffffu, mine, 1);
+        j0 = __shfl_sync(0xffffffffu, mine, 4);
+        j1 = __shfl_sync(0xffffffffu, mine, 5);
+        end0 = __shfl_sync(0xffffffffu, mine, 6);
+        pre_tiles = __shfl_sync(0xffffffffu, mine, 7);
+        pre = __shfl_sync(0xffffffffu, mine, 8);
+        last_sees = __shfl_sync(0xffffffffu, mine, 9) + tokens - 1;
+        two = __shfl_sync(0xffffffffu, mine, 10) & kPaTwo;
+        if (elect_one_lane()) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
+        ++count;
+        more = tokens != 0;
+        in_item = more;
+        has0 = two && end0 > j0;
+        j = j0;
+        slot = two ? (has0 ? 0 : 1) : singles & 1;
+        q = qn;
+        new_q = new_k = true;
+      }
+    }
+    const uint32_t of_slot = slot ? e1 : e0, of_other = slot ? e0 : e1;
+    if (in_item && !(of_slot & kHave)) {
+      const uint32_t kb = kv_full + 8 * k_st;
+      const uint32_t qb = smem_u32(&sm.q_full[q & 1]), qp = (q >> 1) & 1;
+      bool ready = true;
+      if (new_q | new_k) {
+        ready = __all_sync(0xffffffffu, (!new_q || mbar_test_wait(qb, qp)) && (!new_k || mbar_test_wait(kb, k_ph)));
+        if (!ready && !(of_other & kHave)) {
+          ok = ready = pa_wait(qb, qp, abort_flag, status) && pa_wait(kb, k_ph, abort_flag, status);
           if (!ok) break;
         }
-        if (got) {
-          const int mine = lane < 12 ? reinterpret_cast<const int32_t*>(&sm.items[count % kPaItems])[lane] : 0;
-          const int tokens = __shfl_sync(0xffffffffu, mine, 1);
-          j0 = __shfl_sync(0xffffffffu, mine, 4);
-          j1 = __shfl_sync(0xffffffffu, mine, 5);
-          end0 = __shfl_sync(0xffffffffu, mine, 6);
-          pre_tiles = __shfl_sync(0xffffffffu, mine, 7);
-          pre = __shfl_sync(0xffffffffu, mine, 8);
-          last_sees = __shfl_sync(0xffffffffu, mine, 9) + tokens - 1;
-          two = __shfl_sync(0xffffffffu, mine, 10) & kPaTwo;
-          if (elect_one_lane()) mbar_arrive(smem_u32(&sm.item_empty[count % kPaItems]));
-          ++count;
-          more = tokens != 0;
-          in_item = more;
-          has0 = two && end0 > j0;
-          j = j0;
-          slot = two ? (has0 ? 0 : 1) : singles & 1;
-          q = qn;
-          new_q = new_k = true;
-        }
-      }
-      have_s = in_item;
-    }
-    if (have_s && ahead < 2 && !((busy >> slot) & 1)) {
-      const uint32_t kb = smem_u32(&sm.kv_full[ring % kPaStages]), kp = (ring / kPaStages) & 1;
-      const uint32_t qb = smem_u32(&sm.q_full[q & 1]), qp = (q >> 1) & 1;
-      bool ready = (!new_q || __all_sync(0xffffffffu, mbar_test_wait(qb, qp))) &&
-                   (!new_k || __all_sync(0xffffffffu, mbar_test_wait(kb, kp)));
-      if (!ready && ahead == 0) {
-        ok = ready = pa_wait(qb, qp, abort_flag, status) && pa_wait(kb, kp, abort_flag, status);
-        if (!ok) break;
       }
       if (ready) {
         // the last step on this key tile, and on these queries
-        const bool free_k = !two || slot == 1, free_q = two && slot == 0 ? j + 1 == end0 : j + 1 == j1;
+        const bool free_k = !two || slot == 1, free_q = j + 1 == (two && slot == 0 ? end0 : j1);
         const uint64_t q_desc = smem_desc_sw128(q_s + (q & 1) * kPaTileBytes);
-        const uint64_t k_desc = smem_desc_sw128(kv_s + (ring % kPaStages) * kPaTileBytes);
+        const uint64_t k_desc = smem_desc_sw128(kv_s + k_st * kPaTileBytes);
         if (elect_one_lane()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -706,65 +788,58 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
             mma_ss_bf16(tmem + slot * 128, q_desc + off, k_desc + off, kIdescScores, k > 0);
           }
           mma_commit(smem_u32(&sm.s_ready[slot]));
-          if (free_k) mma_commit(smem_u32(&sm.kv_empty[ring % kPaStages]));
+          if (free_k) mma_commit(kv_empty + 8 * k_st);
           if (free_q) mma_commit(smem_u32(&sm.q_empty[q & 1]));
         }
         __syncwarp();
-        const int left = j < pre_tiles ? pre - j * 128 : last_sees - (j - pre_tiles) * 128;
-        const bool first = j == j0 || (!two && j == j0 + 1);
-        const bool last = two ? free_q : j + 2 >= j1;
-        const uint32_t w = static_cast<uint32_t>(min(left, 128)) | (slot ? kSlot : 0) | (first ? kFirst : 0) |
-                           (free_k ? kFree : 0) | (last ? kLast : 0) | (new_k ? kNew : 0);
-        if (ahead == 0) {
-          pv_r[0] = ring + 1;
-          pv_w[0] = w;
-        } else {
-          pv_r[1] = ring + 1;
-          pv_w[1] = w;
-        }
-        ++ahead;
-        busy |= 1u << slot;
+        uint32_t v_st = k_st, v_ph = k_ph;
+        forth(v_st, v_ph, 1);
+        const uint32_t e = kHave | static_cast<uint32_t>(min(tail_of(j), 128)) | v_st * kStage | v_ph * kPhase |
+                           (j == j0 || (!two && j == j0 + 1) ? kFirst : 0) | (free_k ? kFree : 0) |
+                           ((two ? free_q : j + 2 >= j1) ? kLast : 0) | (new_k ? kNew : 0);
+        if (!(of_other & kHave)) oldest = slot;
+        if (slot) e1 = e; else e0 = e;
         // the next step
-        have_s = false;
         new_k = free_k;
+        new_q = two && j == j0 && slot == 0;
         if (two && slot == 0) {
           slot = 1;
           q = qn + 1;
-          new_q = j == j0;
         } else {
-          ring += 2;
-          new_q = false;
+          forth(k_st, k_ph, 2);
           if (++j >= j1) {
             in_item = false;
             qn += has0 ? 2 : 1;
             if (!two) singles += j1 - j0;
           } else if (two) {
             slot = j < end0 ? 0 : 1;
-            q = qn + (slot == 1 && has0);
+            q = qn + (slot & (has0 ? 1 : 0));
           } else {
             slot ^= 1;
           }
         }
-        if (ahead < 2) continue;
+        continue;
       }
     }
-    if (ahead == 0) {
+    if (!((e0 | e1) & kHave)) {
       if (more) continue;
       break;
     }
-    if (two && in_item && ahead == 2 && slot == 0 && !(pv_w[0] & (kFirst | kSlot))) {
-      // The middle of an item with two row tiles, all keys seen: nothing to decide but whether the keys
-      // are there.  P V of tile j - 1 and S of tile j, for slot 0, then for slot 1.
+    if (two && in_item && (e0 & e1 & kHave) && slot == 0 && oldest == 0 && !(e0 & (kFirst | kLast)) &&
+        j + 1 < end0 && (j - 1 >= pre_tiles || j * 128 <= pre)) {
+      // The middle of an item with two row tiles, all keys seen (neither is P V to come the last of an item):
+      // nothing to decide but whether the keys are there.  P V of tile j - 1 and S of tile j, for slot 0,
+      // then for slot 1.
       bool landed = true;
       // A barrier is looked at, and a fence made, while the last two products before are still queued.
       const uint32_t p0 = smem_u32(&sm.p_ready[0]), p1 = smem_u32(&sm.p_ready[1]);
       bool p_there = false;                    // P of the slot at hand is known (and fenced)
-      while (j + 1 < end0 && (j - 1 >= pre_tiles || j * 128 <= pre)) {
-        const uint32_t k_st = ring % kPaStages, v_st = (ring - 1) % kPaStages;
-        const uint32_t kb = smem_u32(&sm.kv_full[k_st]), kp = (ring / kPaStages) & 1;
+      uint32_t v_st = (e0 / kStage) & 7, v_ph = (e0 / kPhase) & 1;
+      do {
+        const uint32_t kb = kv_full + 8 * k_st;
         const uint64_t k_desc = smem_desc_sw128(kv_s + k_st * kPaTileBytes);
         const uint64_t v_desc = smem_desc_rows_n(kv_s + v_st * kPaTileBytes);
-        if (!pa_wait(smem_u32(&sm.kv_full[v_st]), ((ring - 1) / kPaStages) & 1, abort_flag, status)) { ok = false; break; }
+        if (!pa_wait(kv_full + 8 * v_st, v_ph, abort_flag, status)) { ok = false; break; }
 #pragma unroll 1
         for (uint32_t x = 0; x < 2; ++x) {
           if (!p_there) {
@@ -778,11 +853,11 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_ts<false>(tmem + 256 + x * 128, tmem + x * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues, 1);
-            if (x) mma_commit(smem_u32(&sm.kv_empty[v_st]));
+            if (x) mma_commit(kv_empty + 8 * v_st);
           }
           __syncwarp();
           if (x == 0) {
-            landed = __all_sync(0xffffffffu, mbar_test_wait(kb, kp));
+            landed = __all_sync(0xffffffffu, mbar_test_wait(kb, k_ph));
             if (!landed) break;
           }
           if (elect_one_lane()) {
@@ -802,48 +877,46 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
               mma_ss_bf16(tmem + x * 128, q_desc + off, k_desc + off, kIdescScores, 1);
             }
             mma_commit(smem_u32(&sm.s_ready[x]));
-            if (x) mma_commit(smem_u32(&sm.kv_empty[k_st]));
+            if (x) mma_commit(kv_empty + 8 * k_st);
           }
           __syncwarp();
         }
         if (!ok || !landed) break;
+        v_st = k_st;
+        v_ph = k_ph;
+        forth(v_st, v_ph, 1);
+        forth(k_st, k_ph, 2);
         ++j;
-        ring += 2;
-        pv_r[0] = pv_r[1] = ring - 1;
-        pv_w[0] = 128 | kNew;
-        pv_w[1] = 128 | kSlot | kFree;
-      }
+      } while (j + 1 < end0 && (j - 1 >= pre_tiles || j * 128 <= pre));
       if (!ok) break;
+      // tile j - 1 may be the prefix's last
+      const uint32_t e = kHave | static_cast<uint32_t>(min(tail_of(j - 1), 128)) | v_st * kStage | v_ph * kPhase;
+      e0 = e | kNew;
+      e1 = e | kFree;
       if (!landed) {                           // P V of slot 0 is done, that of slot 1 is to come
-        pv_r[0] = pv_r[1];
-        pv_w[0] = pv_w[1];
-        ahead = 1;
-        busy = 2;
-        new_k = true;
-        pv_w[0] &= ~kNew;
+        e0 = 0;
+        oldest = 1;
         continue;
       }
     }
     // O (+)= P V of the oldest S
-    const uint32_t r = pv_r[0], w = pv_w[0];
-    pv_r[0] = pv_r[1];
-    pv_w[0] = pv_w[1];
-    --ahead;
-    const uint32_t ps = w & kSlot ? 1 : 0;
-    const int tail = w & 255;                // the tile's first unseen key (128: none)
-    const uint32_t vb = smem_u32(&sm.kv_full[r % kPaStages]);
-    if ((w & kNew) && !pa_wait(vb, (r / kPaStages) & 1, abort_flag, status)) { ok = false; break; }
-    const uint32_t va = kv_s + (r % kPaStages) * kPaTileBytes;
-    if (w & kFirst) {                        // the item before with steps in the slot has read its O
-      const uint32_t before = ps ? o_count[1]++ : o_count[0]++;
+    const uint32_t ps = oldest, e = ps ? e1 : e0;
+    if (ps) e1 = 0; else e0 = 0;
+    oldest ^= 1;
+    const int tail = e & 255;                  // the tile's first unseen key (128: none)
+    const uint32_t v_st = (e / kStage) & 7;
+    const uint32_t va = kv_s + v_st * kPaTileBytes;
+    if ((e & kNew) && !pa_wait(kv_full + 8 * v_st, (e / kPhase) & 1, abort_flag, status)) { ok = false; break; }
+    if (e & kFirst) {                          // the item before with steps in the slot has read its O
+      const uint32_t before = ps ? o_count1++ : o_count0++;
       if (before > 0 && !pa_wait(smem_u32(&sm.o_free[ps]), (before - 1) & 1, abort_flag, status)) { ok = false; break; }
     }
     const int pv_steps = (tail + 15) >> 4;
     if (tail & 15) {
       // keys past the last one seen may hold anything: their weights are 0, their values are made 0
 #pragma unroll 1
-      for (int e = lane; e < (pv_steps * 16 - tail) * 16; e += 32) {
-        const uint32_t at = va + ((e >> 3) & 1) * (kPaTileBytes / 2) + (tail + (e >> 4)) * 128 + (e & 7) * 16;
+      for (int z = lane; z < (pv_steps * 16 - tail) * 16; z += 32) {
+        const uint32_t at = va + ((z >> 3) & 1) * (kPaTileBytes / 2) + (tail + (z >> 4)) * 128 + (z & 7) * 16;
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
       }
       fence_proxy_async_smem();
@@ -858,12 +931,11 @@ __device__ __forceinline__ void pa_multiply(const PromptArgs& a, PaShared& sm, u
       for (int k = 0; k < 8; ++k)
         if (k < pv_steps)
           mma_ts<false>(tmem + 256 + ps * 128, tmem + ps * 128 + k * 8, v_desc + k * (2048 >> 4), kIdescValues,
-                        k > 0 || !(w & kFirst));
-      if (w & kFree) mma_commit(smem_u32(&sm.kv_empty[r % kPaStages]));
-      if (w & kLast) mma_commit(smem_u32(&sm.pv_done[ps]));
+                        k > 0 || !(e & kFirst));
+      if (e & kFree) mma_commit(kv_empty + 8 * v_st);
+      if (e & kLast) mma_commit(smem_u32(&sm.pv_done[ps]));
     }
     __syncwarp();
-    busy &= ~(1u << ps);
   }
   if (!ok) {
     // given up: the products in flight end before tensor memory goes
@@ -942,13 +1014,15 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         const int at = (in_pre ? j : j - pre_tiles) * 128;
         const bool partly = at + 128 > (in_pre ? pre_sees : own_least);   // some key of the tile is not seen
         const int lim = (in_pre ? pre_sees : own_sees) - at;
+        // Columns from `seen` on no row of the warp sees: neither read nor weighed, their P is 0.  Before
+        // that, where some row does not see some column, -inf goes into S (a small loop for what is rare:
+        // the warps of all roles share the instruction caches).  exp2_poly makes 2^-126 of -inf: nothing
+        // beside the largest weight of any row, and a row without any is known by its m.
+        int seen = 128;
         if (partly) {
-          // the tile's unseen keys, in tensor memory (a small loop for what is rare: the warps of all roles
-          // share the instruction caches).  exp2_poly makes 2^-126 of -inf: nothing beside the largest
-          // weight of any row, and a row without any is known by its m.
+          seen = __reduce_max_sync(0xffffffffu, max(min(lim, 128), 0));
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            if (!__any_sync(0xffffffffu, c + 16 > lim)) continue;
+          for (int c = max(0, __reduce_min_sync(0xffffffffu, lim)) & ~15; c < ((seen + 63) & ~63); c += 16) {
             uint32_t x[16];
             tmem_ld16(s_t + c, x);
             tmem_ld_wait();
@@ -969,14 +1043,15 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         };
         tmem_ld32(s_t, u[0]);
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
+        for (int c = 0; c < seen; c += 64) {
           tmem_ld_wait();
           tmem_ld32(s_t + c + 32, u[1]);
           largest(u[0]);
           tmem_ld_wait();
-          if (c == 0) tmem_ld32(s_t + 64, u[0]);
+          if (c + 64 < seen) tmem_ld32(s_t + 64, u[0]);
           largest(u[1]);
         }
+        tmem_ld_wait();
         tmem_ld32(s_t, u[0]);
         const bool raise = (top - m) * kScoreLog2 > kRaise;           // false where both are -inf
         float f = 1.f;
@@ -1006,11 +1081,20 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         };
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
+          if (c >= seen) {
+            uint32_t none[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) none[e] = 0u;
+            tmem_ld_wait();
+            tmem_st16(s_t + (c >> 1), none);
+            tmem_st16(s_t + (c >> 1) + 16, none);
+            continue;
+          }
           tmem_ld_wait();
           tmem_ld32(s_t + c + 32, u[1]);
           weights(u[0], c);
           tmem_ld_wait();
-          if (c == 0) tmem_ld32(s_t + 64, u[0]);
+          if (c + 64 < seen) tmem_ld32(s_t + 64, u[0]);
           weights(u[1], c + 32);
         }
         if (!fresh && __any_sync(0xffffffffu, f != 1.f)) {
@@ -1071,7 +1155,7 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
     items1 += has1;
     if (!(item.flags & kPaWhole) && (item.flags & kPaEnds) && threadIdx.x == kPaThreads - 128) {
       // the item's last piece is here: what the joining kernel has to know
-      PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x;
+      PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + pa_cta();
       join->first = item.first_cta;
       join->tok = item.tok;
       join->tokens = item.tokens;
@@ -1119,7 +1203,7 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
       } else {
         float2* ml;
         if (!whole) {                                                 // a piece: columns in blocks of 4
-          const int64_t tile = (static_cast<int64_t>(blockIdx.x) * 2 + (item.flags & kPaCarried ? 0 : 1)) * 2 + x;
+          const int64_t tile = (static_cast<int64_t>(pa_cta()) * 2 + (item.flags & kPaCarried ? 0 : 1)) * 2 + x;
           ml = reinterpret_cast<float2*>(a.work + a.off_ml) + tile * 128 + row;
           dst = reinterpret_cast<float*>(a.work + a.off_o) + tile * 128 * kHeadDim + row * 4;
         } else {
@@ -1185,8 +1269,8 @@ __device__ __forceinline__ void pa_refuse(const PromptArgs& a) {
   const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   const bool no_prefix = pa_prefix(a) < 0;
-  if (no_prefix && blockIdx.x == 0 && lane == 0) atomicOr(status, kDevBadInput);
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+  if (no_prefix && pa_cta() == 0 && lane == 0) atomicOr(status, kDevBadInput);
+  for (int b = pa_cta(); b < a.batch; b += gridDim.x * gridDim.y) {
     const PaSequence s = pa_sequence(a, b);
     if (!s.bad && !no_prefix) continue;
     if (s.bad && lane == 0) atomicOr(status, kDevBadInput);
@@ -1243,9 +1327,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // Nothing of this call is read or written before the kernels ahead of it are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + blockIdx.x)->valid = 0;
+  if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + pa_cta())->valid = 0;
   tc_fence_before();
-  if (a.batch > kPaWarpBatch) {
+  if (a.batch > kPaWarpBatch && a.parts == 0) {
     __syncthreads();
     pa_find_share(a, sm);
   } else if (warp != 10) {

@@ -208,6 +208,9 @@ PREFIX = [
     (3, [4, 8], 4, 2, 0),
     ([3, 0, 90, 1, 300], [0, 5, 0, 77, 10], 8, 2, 640),
     ([1] * 300, [7] * 300, 4, 2, 2000),
+    ([700, 5], [0, 9], 2, 1, 900),            # long runs behind a prefix that ends inside a tile
+    ([1200], [300], 8, 8, 400),
+    (300, [0, 130, 70], 4, 4, 1050),
 ]
 
 
