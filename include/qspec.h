@@ -423,7 +423,7 @@ qspec_status qspec_attn_prefix(const uint16_t* q, int64_t ld_q, int64_t n_tokens
 
 /* Bytes of workspace on the current device (0: invalid arguments or device). */
 size_t qspec_attn_prefill_workspace_size(void);
-size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q);
+size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q, int32_t h_kv);
 
 /*
  * W4A16 verifying GEMM that allocates nothing and takes no workspace.

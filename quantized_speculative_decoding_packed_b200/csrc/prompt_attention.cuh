@@ -14,7 +14,7 @@
 // A CTA per SM works through its share of the items (prompt_schedule.cuh).
 //   warp 10: finds the share's items and passes them on (ring of 4);
 //   warp 8: TMA of queries (ring of two tiles) and of key and value tiles
-//           (ring of 5 x 32 KB);
+//           (ring of 4 x 32 KB);
 //   warp 9: tcgen05.mma: S of the next step before P V of the current one;
 //   warps 0-3, 4-7: the softmax of slots 0 and 1, a thread for each row.  A slot
 //           is a tile of S, and of O, in tensor memory; P takes S's place;
@@ -37,7 +37,7 @@
 
 namespace qspec {
 
-constexpr int kPaStages = 5;
+constexpr int kPaStages = 4;
 constexpr int kPaItems = 4;                                  // items passed on ahead
 constexpr int kPaThreads = 512;
 constexpr int kPaTileBytes = 128 * kHeadDim * 2;             // 32 KB: a tile of Q, K or V
@@ -57,6 +57,7 @@ struct PromptArgs {
   int64_t ld_out;
   int64_t off_owners, off_desc, off_ml, off_o, off_row_ml, off_row_o;
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
+  int ctas;                    // of the attention's grid
   int parts;                   // > 0: few items, each has so many CTAs of its own (grid: parts x items)
 };
 
@@ -1458,6 +1459,9 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   const int in0 = tok % (2 * a.tpt), in1 = t < 2 * a.tpt ? t : t % (2 * a.tpt);     // the token's place in its item
   const int2 c0 = prefix > 0 ? owners[static_cast<int64_t>(tok - in0) * a.h_kv + g] : make_int2(0, -1);
   const int2 c1 = owners[static_cast<int64_t>(a.n_tok) * a.h_kv + static_cast<int64_t>(tok - in1) * a.h_kv + g];
+  // (what a call that gave up, or whose starts are not in order, has left out is not followed)
+  auto sound = [&](int2 c) { return c.x >= 0 && c.x <= c.y && c.y < a.ctas; };
+  if ((prefix > 0 && !sound(c0)) || !sound(c1)) return;
   const int n0 = c0.y - c0.x + 1, n = n0 + c1.y - c1.x + 1;
   const int in_group = head - g * a.group;
   float m = -INFINITY, l = 0.f;

@@ -430,6 +430,10 @@ bool make_kv_tmap(CUtensorMap* map, const uint16_t* base, uint64_t heads, uint64
   return make_tmap_bf16<4>(map, base, dims, strides, box);
 }
 
+int prompt_mode(int64_t n_tok, int32_t batch, int32_t group, bool with_prefix) {
+  return !with_prefix ? kPaNoPrefix : (n_tok / batch * group >= kPaAheadRows ? kPaPrefixAhead : kPaPrefixOnce);
+}
+
 // The attention of many tokens, with or without a shared prefix.
 qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok, int32_t batch, const int32_t* cu,
                                   int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens, int32_t offset,
@@ -457,7 +461,10 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   qspec_status st = current_device(&dev, &info);
   if (st != QSPEC_OK) return st;
   const int grid = info.sm_count;
-  const PaLayout lay = pa_layout(grid, n_tok * h_q, n_tok * h_q, with_prefix);
+  // A sequence's own rows fill a row tile (on average): the prefix goes ahead of its keys, in the
+  // same items, and nothing is left to join but what is split.
+  const int mode = prompt_mode(n_tok, batch, group, with_prefix);
+  const PaLayout lay = pa_layout(grid, n_tok * h_kv, n_tok * h_q, mode == kPaPrefixOnce);
   if (workspace_bytes < static_cast<size_t>(lay.total)) return QSPEC_ERR_WORKSPACE_TOO_SMALL;
   static std::atomic<bool> attr_set[kMaxDevices];
   if (!attr_set[dev].load(std::memory_order_acquire)) {
@@ -491,9 +498,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.tpt = 128 / group;
   a.l_max = l_max;
   a.prefix_max = with_prefix ? prefix_max : 0;
-  // A sequence's own rows fill a row tile (on average): the prefix goes ahead of its keys, in the
-  // same items, and nothing is left to join but what is split.
-  a.mode = !with_prefix ? kPaNoPrefix : (n_tok / batch * group >= kPaAheadRows ? kPaPrefixAhead : kPaPrefixOnce);
+  a.mode = mode;
   // Few items (by what the host knows: at most so many, of at most so many key tiles): a CTA takes one, or
   // a part of one, which it finds at once.  Else the shares of prompt_schedule.cuh.  (Measured for one
   // prompt of 200 tokens, 32 heads over 8: 13.3 us against 19.4.)
@@ -503,6 +508,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.parts = batch <= 32 && items <= grid ? static_cast<int>(grid / items) : 0;
   if (a.parts > (most_tiles + 3) / 4) a.parts = static_cast<int>((most_tiles + 3) / 4);
   const dim3 shape = a.parts > 0 ? dim3(static_cast<unsigned>(a.parts), static_cast<unsigned>(items)) : dim3(static_cast<unsigned>(grid));
+  a.ctas = static_cast<int>(shape.x * shape.y);
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
   const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};
@@ -882,13 +888,14 @@ size_t qspec_attn_prefill_workspace_size(void) {
   return static_cast<size_t>(pa_layout(info.sm_count, 0, 0, false).total);
 }
 
-size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q) {
+size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q, int32_t h_kv) {
   if (n_tokens < 1 || n_tokens > 0x7FFFFFFFll - 256 || batch < 1 || batch > 65535 || h_q < 1 || h_q > (1 << 20) ||
-      n_tokens * h_q > (1ll << 33))
+      h_kv < 1 || h_q % h_kv != 0 || h_q / h_kv > 128 || n_tokens * h_q > (1ll << 33))
     return 0;
   DeviceInfo info;
   if (current_device(nullptr, &info) != QSPEC_OK) return 0;
-  return static_cast<size_t>(pa_layout(info.sm_count, n_tokens * h_q, n_tokens * h_q, true).total);
+  const bool rows = prompt_mode(n_tokens, batch, h_q / h_kv, true) == kPaPrefixOnce;
+  return static_cast<size_t>(pa_layout(info.sm_count, n_tokens * h_kv, n_tokens * h_q, rows).total);
 }
 
 qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,

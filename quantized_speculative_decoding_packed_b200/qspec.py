@@ -84,7 +84,7 @@ def _load() -> ctypes.CDLL:
                                       P, I64, P, SZ, P]
     lib.qspec_attn_prefill_workspace_size.argtypes = []
     lib.qspec_attn_prefill_workspace_size.restype = SZ
-    lib.qspec_attn_prefix_workspace_size.argtypes = [I64, I32, I32]
+    lib.qspec_attn_prefix_workspace_size.argtypes = [I64, I32, I32, I32]
     lib.qspec_attn_prefix_workspace_size.restype = SZ
     lib.qspec_status_string.argtypes = [I32]
     lib.qspec_status_string.restype = ctypes.c_char_p
@@ -491,7 +491,7 @@ def _new_prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
     return ws
 
 
-PROMPT_WORKSPACE_ZERO = 16384     # bytes of a prompt attention workspace that start as zeros
+PROMPT_WORKSPACE_ZERO = 256       # bytes of a prompt attention workspace that start as zeros
 
 
 def prompt_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
@@ -531,8 +531,8 @@ def attn_prefill_workspace_size() -> int:
     return size
 
 
-def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int) -> int:
-    return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q))
+def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int, h_kv: int) -> int:
+    return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q, h_kv))
 
 
 def _cache_on(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int):
@@ -665,7 +665,7 @@ def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
         out = torch.empty((n, cols), dtype=_BF16, device=q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = _prompt_workspace(attn_prefix_workspace_size(n, b, h_q), dev, handle)
+        work = _prompt_workspace(attn_prefix_workspace_size(n, b, h_q, h_kv), dev, handle)
     _check(LIB.qspec_attn_prefix(_rows(q, _BF16, dev, n, cols, "q"), q.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM,
                                  lens_p, offset, kc, vc, l_max, _on(prefix_k, _BF16, dev, "prefix_k"),
                                  _on(prefix_v, _BF16, dev, "prefix_v"), prefix_k.shape[1], _one(prefix_len, dev),

@@ -247,7 +247,7 @@ def test_prefix_refuses_bad_lengths_on_the_device(qs):
     new, old, h_q, h_kv, plen = [2] * 3, [20, 7, 130], 4, 2, 200
     q, kc, vc, cu, lens = _case(9, new, old, h_q, h_kv)
     pk, pv = _prefix(10, h_kv, plen)
-    size = qs.attn_prefix_workspace_size(6, 3, h_q)
+    size = qs.attn_prefix_workspace_size(6, 3, h_q, h_kv)
     for bad in (-1, pk.shape[1] + 1):
         work = torch.zeros(size, dtype=torch.uint8, device="cuda")
         out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([bad]), work=work)
@@ -425,3 +425,148 @@ def test_rope_skips_positions_outside(qs):
     assert qs.workspace_status(work) == BAD_INPUT
     qs.qkv_rope_append(qkv, _i32([0, 0]), 0, kc, vc, h_q, _table(qs, 128, 64), prefix_len=_i32([-1]), work=work)
     assert qs.workspace_status(work) == BAD_INPUT
+
+
+# ---------------------------------------------------------------- as they are used
+def test_two_streams_and_graphs(qs):
+    """Calls on two streams at once have workspaces of their own; captured calls give what eager ones give, on
+    new inputs in the captured buffers, beside eager calls."""
+    new, old, h_q, h_kv, plen = [40, 300, 7], [3, 0, 200], 8, 2, 500
+    sets = [_case(30 + i, new, old, h_q, h_kv) for i in range(2)]
+    pk, pv = _prefix(40, h_kv, plen)
+    plen_d = _i32([plen])
+
+    def both(i):
+        q, kc, vc, cu, lens = sets[i]
+        return (qs.attn_prefill(q, cu, lens, kc, vc, h_q),
+                qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, plen_d, cu=cu),
+                qs.attn_prefix(q[:3], lens, 0, kc, vc, h_q, pk, pv, plen_d))
+
+    want = [both(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(both(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
+    q, kc, vc, cu, lens = [x.clone() for x in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = (qs.attn_prefill(q, cu, lens, kc, vc, h_q), qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, plen_d, cu=cu),
+                qs.attn_prefix(q[:3], lens, 0, kc, vc, h_q, pk, pv, plen_d))
+    for i in (1, 0, 1):
+        for dst, src in zip((q, kc, vc, cu, lens), sets[i]):
+            dst.copy_(src)
+        graph.replay()
+        eager = both(i)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want[i]))
+        assert all(torch.equal(x, y) for x, y in zip(eager, want[i]))
+
+
+def test_default_workspace_grows_and_is_kept(qs):
+    """A larger call after a captured one: the graph's own buffer is untouched, the eager one is replaced."""
+    h_q, h_kv, plen = 4, 2, 100
+    pk, pv = _prefix(41, h_kv, plen)
+    small = _case(42, [1] * 4, [9] * 4, h_q, h_kv)
+    big = _case(43, [1] * 400, [30] * 400, h_q, h_kv)
+    call = lambda c: qs.attn_prefix(c[0], c[4], 0, c[1], c[2], h_q, pk, pv, _i32([plen]))   # noqa: E731
+    want = call(small)
+    _check(call(big), [1] * 400, [30] * 400, big[0], big[1], big[2], h_q, pk, pv, plen)
+    assert torch.equal(call(small), want)
+
+
+def test_prompts_then_rounds_behind_a_prefix(qs):
+    """A prefix and prompts are read in, then drafting and verifying passes run, all through one cache: every
+    attention against 64 bits from the same cache, the cache and the lengths as the calls say."""
+    g = _gen(50)
+    h_q, h_kv, batch, gamma, plen, l_max = 8, 2, 3, 2, 77, 200
+    width = (h_q + 2 * h_kv) * D
+    table = _table(qs, 128, plen + l_max)
+    qg, kg = _randn(g, D, dtype=torch.float32), _randn(g, D, dtype=torch.float32)
+    # the prefix: a cache of one sequence
+    pk = torch.zeros(1, h_kv, 128, D, dtype=torch.bfloat16, device="cuda")
+    pv = torch.zeros_like(pk)
+    zero = _i32([0])
+    qkv = _randn(g, plen, width, dtype=torch.float32)
+    q = qs.qkv_rope_append(qkv, zero, 0, pk, pv, h_q, table, cu=_i32([0, plen]), q_gamma=qg, k_gamma=kg)
+    out = qs.attn_prefill(q, _i32([0, plen]), zero, pk, pv, h_q)
+    _check(out, [plen], [0], q, pk, pv, h_q)
+    # the prompts behind it (one slot has none)
+    kc = torch.zeros(batch, h_kv, l_max, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    lens, plen_d = _i32([0] * batch), _i32([plen])
+    new = [30, 0, 95]
+    cu = _i32(_starts(new))
+    qkv = _randn(g, sum(new), width, dtype=torch.float32)
+    q = qs.qkv_rope_append(qkv, lens, 0, kc, vc, h_q, table, cu=cu, prefix_len=plen_d, q_gamma=qg, k_gamma=kg)
+    ref, mag = _rope64(qkv.view(-1, h_q + 2 * h_kv, D)[:, :h_q], qg, 1e-6, table,
+                       plen + torch.cat([torch.arange(m, device="cuda") for m in new]), False)
+    assert bool(((q.view(-1, h_q, D).double() - ref).abs() <= 24 * 2.0 ** -24 * mag + 1.001 * 2.0 ** -8 * ref.abs()).all())
+    out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk[0], pv[0], plen_d, cu=cu)
+    _check(out, new, [0] * batch, q, kc, vc, h_q, pk[0], pv[0], plen)
+    n_acc = _i32([m - 1 for m in new])
+    work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qs.kv_commit(lens, n_acc, l_max, work=work)
+    assert qs.workspace_status(work) == BAD_INPUT          # the slot without a prompt is left as it was
+    assert lens.tolist() == new
+    at = list(new)
+    for accepted in ([2, 0, 1], [0, 1, 2]):
+        for j in range(gamma):                             # drafting: one token each
+            qkv = _randn(g, batch, width, dtype=torch.float32)
+            q = qs.qkv_rope_append(qkv, lens, j, kc, vc, h_q, table, prefix_len=plen_d, q_gamma=qg, k_gamma=kg)
+            out = qs.attn_prefix(q, lens, j, kc, vc, h_q, pk[0], pv[0], plen_d)
+            _check(out, [1] * batch, [x + j for x in at], q, kc, vc, h_q, pk[0], pv[0], plen)
+        qkv = _randn(g, batch * (gamma + 1), width, dtype=torch.float32)      # verifying: gamma + 1 tokens each
+        q = qs.qkv_rope_append(qkv, lens, 0, kc, vc, h_q, table, prefix_len=plen_d, q_gamma=qg, k_gamma=kg)
+        out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk[0], pv[0], plen_d)
+        _check(out, [gamma + 1] * batch, at, q, kc, vc, h_q, pk[0], pv[0], plen)
+        qs.kv_commit(lens, _i32(accepted), l_max)
+        at = [x + y + 1 for x, y in zip(at, accepted)]
+        assert lens.tolist() == at
+
+
+def test_many_sequences(qs):
+    """More sequences than one warp, and than a CTA, looks after; most without tokens."""
+    for batch, seed in ((70, 60), (1500, 61)):
+        r = torch.Generator().manual_seed(seed)
+        new = [int(x) if int(x) < 9 else 0 for x in torch.randint(0, 30, (batch,), generator=r)]
+        old = [int(x) for x in torch.randint(0, 40, (batch,), generator=r)]
+        h_q, h_kv = 2, 1
+        q, kc, vc, cu, lens = _case(seed, new, old, h_q, h_kv)
+        out = qs.attn_prefill(q, cu, lens, kc, vc, h_q)
+        _check(out, new, old, q, kc, vc, h_q)
+        pk, pv = _prefix(seed, h_kv, 150)
+        out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([150]), cu=cu)
+        _check(out, new, old, q, kc, vc, h_q, pk, pv, 150)
+
+
+def test_long_context_single_token(qs):
+    """One token behind 300000 keys: many pieces of one item."""
+    old, h_q, h_kv = [300000], 4, 2
+    q, kc, vc, cu, lens = _case(62, [1], old, h_q, h_kv)
+    out = qs.attn_prefill(q, cu, lens, kc, vc, h_q)
+    _check(out, [1], old, q, kc, vc, h_q)
+    pk, pv = _prefix(63, h_kv, 250000)
+    out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([250000]))
+    _check(out, [1], old, q, kc, vc, h_q, pk, pv, 250000)
+
+
+def test_binding_refuses(qs):
+    q, kc, vc, cu, lens = _case(64, [4, 5], [0, 3], 4, 2)
+    for bad in (dict(cu=cu[:2]), dict(lens=lens[:1]), dict(q=q.float()), dict(q=q[:, :256]), dict(kc=kc.float()),
+                dict(kc=kc[:, :, ::2]), dict(out=torch.empty(8, 512, dtype=torch.bfloat16, device="cuda")),
+                dict(lens=lens.cpu()), dict(cu=cu.long()), dict(cu=None)):
+        a = dict(q=q, cu=cu, lens=lens, kc=kc, vc=vc, out=None)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            qs.attn_prefill(a["q"], a["cu"], a["lens"], a["kc"], a["vc"], 4, out=a["out"])
+    with pytest.raises(qs.QSpecError):
+        qs.attn_prefill(q, cu, lens, kc, vc, 4, out=q)                        # over the queries
+    with pytest.raises(qs.QSpecError):
+        qs.attn_prefill(q, cu, lens, kc, vc, 4, work=torch.zeros(4096, dtype=torch.uint8, device="cuda"))

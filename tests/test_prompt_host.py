@@ -102,8 +102,9 @@ def test_prefix_rejects(lib, kw):
 
 
 def test_workspace_sizes_refuse_bad_shapes(lib):
-    for n, b, h in ((0, 1, 1), (1, 0, 1), (1, 65536, 1), (1, 1, 0), (2 ** 31, 1, 1), (2 ** 30, 1, 64)):
-        assert lib.attn_prefix_workspace_size(n, b, h) == 0
+    for n, b, h, kv in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 65536, 1, 1), (1, 1, 0, 1), (2 ** 31, 1, 1, 1), (2 ** 30, 1, 64, 8),
+                        (1, 1, 4, 0), (1, 1, 4, 3), (1, 1, 129, 1)):
+        assert lib.attn_prefix_workspace_size(n, b, h, kv) == 0
 
 
 def test_binding_checks_its_tensors(lib):
