@@ -421,6 +421,17 @@ qspec_status qspec_attn_prefix(const uint16_t* q, int64_t ld_q, int64_t n_tokens
                                const int32_t* prefix_len, uint16_t* out, int64_t ld_out, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* The three calls above with their arguments in one block, for bindings in which every argument
+ * of a call costs time: `args` holds, in the order of the call's parameters without `stream`,
+ * an int64 for each integer and pointer and a double for `eps`; n_args is their number.
+ * QSPEC_ERR_INVALID_ARG where that is another, or an integer does not fit its parameter. */
+enum {
+  QSPEC_CALL_QKV_ROPE_APPEND = 0,   /* 25 arguments */
+  QSPEC_CALL_ATTN_PREFILL = 1,      /* 16 */
+  QSPEC_CALL_ATTN_PREFIX = 2        /* 21 */
+};
+qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* stream);
+
 /* Bytes of workspace on the current device (0: invalid arguments or device). */
 size_t qspec_attn_prefill_workspace_size(void);
 size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q, int32_t h_kv);

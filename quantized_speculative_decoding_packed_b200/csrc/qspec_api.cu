@@ -529,6 +529,32 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   return launch_dependent(prefix_join_kernel, dim3(static_cast<unsigned>((n_tok * h_q + 7) / 8)), 256, 0, stream, a);
 }
 
+// The arguments of qspec_call, one after another.
+struct PackedArgs {
+  const uint8_t* at;
+  bool ok = true;
+  int64_t next() {
+    int64_t v;
+    std::memcpy(&v, at, 8);
+    at += 8;
+    return v;
+  }
+  int32_t i32() {
+    const int64_t v = next();
+    ok = ok && v >= INT32_MIN && v <= INT32_MAX;
+    return static_cast<int32_t>(v);
+  }
+  template <typename T>
+  T* ptr() {
+    return reinterpret_cast<T*>(static_cast<uintptr_t>(next()));
+  }
+  float real() {
+    double v;
+    std::memcpy(&v, at, 8);
+    at += 8;
+    return static_cast<float>(v);
+  }
+};
 }  // namespace
 }  // namespace qspec
 
@@ -916,6 +942,64 @@ qspec_status qspec_attn_prefix(const uint16_t* q, int64_t ld_q, int64_t n_tokens
   return run_prompt_attention(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, offset, k_cache, v_cache, l_max,
                               true, prefix_k, prefix_v, prefix_max, prefix_len, out, ld_out, workspace,
                               workspace_bytes, stream);
+}
+
+qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* stream) {
+  if (!args) return QSPEC_ERR_INVALID_ARG;
+  PackedArgs p{static_cast<const uint8_t*>(args)};
+  if (call == QSPEC_CALL_QKV_ROPE_APPEND && n_args == 25) {
+    const float* qkv = p.ptr<const float>();
+    const int64_t ld_qkv = p.next(), n_tokens = p.next();
+    const int32_t batch = p.i32();
+    const int32_t* cu = p.ptr<const int32_t>();
+    const int32_t h_q = p.i32(), h_kv = p.i32(), head_dim = p.i32();
+    const float* q_gamma = p.ptr<const float>();
+    const float* k_gamma = p.ptr<const float>();
+    const float eps = p.real();
+    const float* table = p.ptr<const float>();
+    const int64_t positions = p.next();
+    const int32_t rot = p.i32();
+    const int32_t* prefix_len = p.ptr<const int32_t>();
+    const int32_t* lens = p.ptr<const int32_t>();
+    const int32_t offset = p.i32();
+    uint16_t* k_cache = p.ptr<uint16_t>();
+    uint16_t* v_cache = p.ptr<uint16_t>();
+    const int32_t l_max = p.i32();
+    void* q_out = p.ptr<void>();
+    const int64_t ld_q = p.next(), flags = p.next();
+    void* workspace = p.ptr<void>();
+    const int64_t bytes = p.next();
+    if (!p.ok || flags < 0 || flags > UINT32_MAX || bytes < 0) return QSPEC_ERR_INVALID_ARG;
+    return qspec_qkv_rope_append(qkv, ld_qkv, n_tokens, batch, cu, h_q, h_kv, head_dim, q_gamma, k_gamma, eps, table,
+                                 positions, rot, prefix_len, lens, offset, k_cache, v_cache, l_max, q_out, ld_q,
+                                 static_cast<uint32_t>(flags), workspace, static_cast<size_t>(bytes), stream);
+  }
+  const bool prefix = call == QSPEC_CALL_ATTN_PREFIX && n_args == 21;
+  if (!prefix && !(call == QSPEC_CALL_ATTN_PREFILL && n_args == 16)) return QSPEC_ERR_INVALID_ARG;
+  const uint16_t* q = p.ptr<const uint16_t>();
+  const int64_t ld_q = p.next(), n_tokens = p.next();
+  const int32_t batch = p.i32();
+  const int32_t* cu = p.ptr<const int32_t>();
+  const int32_t h_q = p.i32(), h_kv = p.i32(), head_dim = p.i32();
+  const int32_t* lens = p.ptr<const int32_t>();
+  const int32_t offset = prefix ? p.i32() : 0;
+  const uint16_t* k_cache = p.ptr<const uint16_t>();
+  const uint16_t* v_cache = p.ptr<const uint16_t>();
+  const int32_t l_max = p.i32();
+  const uint16_t* prefix_k = prefix ? p.ptr<const uint16_t>() : nullptr;
+  const uint16_t* prefix_v = prefix ? p.ptr<const uint16_t>() : nullptr;
+  const int32_t prefix_max = prefix ? p.i32() : 0;
+  const int32_t* prefix_len = prefix ? p.ptr<const int32_t>() : nullptr;
+  uint16_t* out = p.ptr<uint16_t>();
+  const int64_t ld_out = p.next();
+  void* workspace = p.ptr<void>();
+  const int64_t bytes = p.next();
+  if (!p.ok || bytes < 0) return QSPEC_ERR_INVALID_ARG;
+  return prefix ? qspec_attn_prefix(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, offset, k_cache, v_cache,
+                                    l_max, prefix_k, prefix_v, prefix_max, prefix_len, out, ld_out, workspace,
+                                    static_cast<size_t>(bytes), stream)
+                : qspec_attn_prefill(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, k_cache, v_cache, l_max,
+                                     out, ld_out, workspace, static_cast<size_t>(bytes), stream);
 }
 
 size_t qspec_workspace_size(int32_t op, int64_t m, int64_t n, int64_t k, int32_t group,

@@ -10,7 +10,9 @@ launch on the current torch stream unless `stream` is given.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -30,7 +32,7 @@ EXPORTED = ("qspec_quantize_weights", "qspec_quant_act", "qspec_cast_bf16", "qsp
             "qspec_kv_append", "qspec_attn_decode", "qspec_attn_workspace_size", "qspec_kv_commit",
             "qspec_rope_table", "qspec_qkv_rope_append", "qspec_attn_prefill",
             "qspec_attn_prefill_workspace_size", "qspec_attn_prefix",
-            "qspec_attn_prefix_workspace_size", "qspec_abi_version")
+            "qspec_attn_prefix_workspace_size", "qspec_call", "qspec_abi_version")
 ABI_VERSION = 5
 HEAD_DIM = 128           # the KV-cache calls' head dimension
 ROPE_INTERLEAVED, ROPE_Q_FP32 = 1, 2
@@ -82,6 +84,7 @@ def _load() -> ctypes.CDLL:
     lib.qspec_attn_prefill.argtypes = [P, I64, I64, I32, P, I32, I32, I32, P, P, P, I32, P, I64, P, SZ, P]
     lib.qspec_attn_prefix.argtypes = [P, I64, I64, I32, P, I32, I32, I32, P, I32, P, P, I32, P, P, I32, P,
                                       P, I64, P, SZ, P]
+    lib.qspec_call.argtypes = [I32, ctypes.c_char_p, I32, P]
     lib.qspec_attn_prefill_workspace_size.argtypes = []
     lib.qspec_attn_prefill_workspace_size.restype = SZ
     lib.qspec_attn_prefix_workspace_size.argtypes = [I64, I32, I32, I32]
@@ -94,7 +97,7 @@ def _load() -> ctypes.CDLL:
                  "qspec_workspace_status",
                  "qspec_gemm_w4a16_noalloc", "qspec_gemm_w4a16_noalloc_status",
                  "qspec_kv_append", "qspec_attn_decode", "qspec_kv_commit", "qspec_rope_table",
-                 "qspec_qkv_rope_append", "qspec_attn_prefill", "qspec_attn_prefix"):
+                 "qspec_qkv_rope_append", "qspec_attn_prefill", "qspec_attn_prefix", "qspec_call"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.qspec_abi_version() != ABI_VERSION:
         raise ImportError(f"{_LIB_PATH} has ABI version {lib.qspec_abi_version()}, "
@@ -446,9 +449,11 @@ def kv_commit(lens: torch.Tensor, n_accepted: torch.Tensor, l_max: int,
 # ---------------------------------------------------------------- the prompt path
 # These calls run thousands of times a second for single tokens, so what they do on the host
 # is kept short: the current stream is asked for as a plain handle (3 us less than the Stream
-# object), pointers go to the library as integers.
+# object), and the arguments go to the library in one block (qspec_call; 25 arguments of a
+# ctypes call take 3 us).
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_ROPE_ARGS, _PREFILL_ARGS, _PREFIX_ARGS = (struct.Struct(f) for f in ("10qd14q", "16q", "21q"))
 
 
 def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
@@ -459,13 +464,19 @@ def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, dtype, dev: int, rows: int, columns: int, name: str) -> int:
-    """The address of a [rows][>= columns] tensor with unit column stride."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be a {dtype} tensor [tokens][columns] with unit column stride on cuda:{dev}")
-    if t.shape[0] != rows or t.shape[1] < columns:
-        raise ValueError(f"{name} must be [{rows}][{columns}], not {list(t.shape)}")
-    return t.data_ptr()
+def _rows(t: torch.Tensor, dtype, dev: int, rows: int, columns: int, name: str):
+    """(address, row stride) of a [rows][>= columns] tensor with unit column stride."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{dev}, not {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < columns:
+        raise ValueError(f"{name} must be [{rows}][{columns}], not {list(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    ld, step = t.stride()
+    if step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld
 
 
 def _current_device(t: torch.Tensor) -> int:
@@ -519,20 +530,20 @@ def _prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
     return cur
 
 
-_PREFILL_WS_SIZE: dict = {}
-
-
 def attn_prefill_workspace_size() -> int:
     """Bytes that attn_prefill needs on the current device (0 where it does not run)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    size = _PREFILL_WS_SIZE.get(dev)
-    if size is None:
-        size = _PREFILL_WS_SIZE[dev] = int(LIB.qspec_attn_prefill_workspace_size())
-    return size
+    return int(LIB.qspec_attn_prefill_workspace_size())
 
 
 def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int, h_kv: int) -> int:
+    """Bytes that attn_prefix needs on the current device (0: invalid shape, or it does not run)."""
     return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q, h_kv))
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt_workspace_size(dev: int, *shape) -> int:
+    """One of the sizes above, for the device `dev`, which is current."""
+    return attn_prefix_workspace_size(*shape) if shape else attn_prefill_workspace_size()
 
 
 def _cache_on(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int):
@@ -550,7 +561,7 @@ def _packed_on(cu, lens: torch.Tensor, batch: int, n_tokens: int, dev: int):
     if cu is None:
         if n_tokens == 0 or n_tokens % batch != 0:
             raise ValueError(f"{n_tokens} rows are not a positive multiple of the batch {batch}")
-        return _on(lens, _I32, dev, "lens"), None
+        return _on(lens, _I32, dev, "lens"), 0
     if cu.numel() != batch + 1:
         raise ValueError(f"cu has {cu.numel()} entries, {batch + 1} are needed")
     return _on(lens, _I32, dev, "lens"), _on(cu, _I32, dev, "cu")
@@ -593,14 +604,14 @@ def qkv_rope_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache:
     dev = _current_device(qkv)
     kc, vc, b, h_kv, l_max = _cache_on(k_cache, v_cache, dev)
     n = qkv.shape[0]
-    x = _rows(qkv, _F32, dev, n, (h_q + 2 * h_kv) * HEAD_DIM, "qkv")
+    x, ld_qkv = _rows(qkv, _F32, dev, n, (h_q + 2 * h_kv) * HEAD_DIM, "qkv")
     lens_p, cu_p = _packed_on(cu, lens, b, n, dev)
     rot = positions = 0
-    angles = None
+    angles = 0
     if table is not None:
         positions, rot = table.shape
         angles = _on(table, _F32, dev, "table")
-    gammas = [None, None]
+    gammas = [0, 0]
     for i, gamma in enumerate((q_gamma, k_gamma)):
         if gamma is not None:
             if gamma.numel() != HEAD_DIM:
@@ -611,12 +622,14 @@ def qkv_rope_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache:
     if q_out.dtype is not _BF16 and q_out.dtype is not _F32:
         raise ValueError("q_out must be bf16 or fp32")
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_Q_FP32 if q_out.dtype is _F32 else 0)
-    _check(LIB.qspec_qkv_rope_append(
-        x, qkv.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM, gammas[0], gammas[1], eps, angles, positions, rot,
-        None if prefix_len is None else _one(prefix_len, dev), lens_p, offset, kc, vc, l_max,
-        _rows(q_out, q_out.dtype, dev, n, h_q * HEAD_DIM, "q_out"), q_out.stride(0), flags,
-        None if work is None else _on(work, torch.uint8, dev, "work"), 0 if work is None else work.numel(),
-        _raw_stream(dev) if stream is None else stream.cuda_stream), "qspec_qkv_rope_append")
+    q_p, ld_q = _rows(q_out, q_out.dtype, dev, n, h_q * HEAD_DIM, "q_out")
+    args = _ROPE_ARGS.pack(
+        x, ld_qkv, n, b, cu_p, h_q, h_kv, HEAD_DIM, gammas[0], gammas[1], eps, angles, positions, rot,
+        0 if prefix_len is None else _one(prefix_len, dev), lens_p, offset, kc, vc, l_max,
+        q_p, ld_q, flags,
+        0 if work is None else _on(work, torch.uint8, dev, "work"), 0 if work is None else work.numel())
+    _check(LIB.qspec_call(0, args, 25, _raw_stream(dev) if stream is None else stream.cuda_stream),
+           "qspec_qkv_rope_append")
     return q_out
 
 
@@ -638,10 +651,12 @@ def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache:
         out = torch.empty((n, cols), dtype=_BF16, device=q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = _prompt_workspace(attn_prefill_workspace_size(), dev, handle)
-    _check(LIB.qspec_attn_prefill(_rows(q, _BF16, dev, n, cols, "q"), q.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM,
-                                  lens_p, kc, vc, l_max, _rows(out, _BF16, dev, n, cols, "out"), out.stride(0),
-                                  _on(work, torch.uint8, dev, "work"), work.numel(), handle), "qspec_attn_prefill")
+        work = _prompt_workspace(_prompt_workspace_size(dev), dev, handle)
+    q_p, ld_q = _rows(q, _BF16, dev, n, cols, "q")
+    out_p, ld_out = _rows(out, _BF16, dev, n, cols, "out")
+    args = _PREFILL_ARGS.pack(q_p, ld_q, n, b, cu_p, h_q, h_kv, HEAD_DIM, lens_p, kc, vc, l_max, out_p, ld_out,
+                              _on(work, torch.uint8, dev, "work"), work.numel())
+    _check(LIB.qspec_call(1, args, 16, handle), "qspec_attn_prefill")
     return out
 
 
@@ -665,10 +680,12 @@ def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
         out = torch.empty((n, cols), dtype=_BF16, device=q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = _prompt_workspace(attn_prefix_workspace_size(n, b, h_q, h_kv), dev, handle)
-    _check(LIB.qspec_attn_prefix(_rows(q, _BF16, dev, n, cols, "q"), q.stride(0), n, b, cu_p, h_q, h_kv, HEAD_DIM,
-                                 lens_p, offset, kc, vc, l_max, _on(prefix_k, _BF16, dev, "prefix_k"),
-                                 _on(prefix_v, _BF16, dev, "prefix_v"), prefix_k.shape[1], _one(prefix_len, dev),
-                                 _rows(out, _BF16, dev, n, cols, "out"), out.stride(0),
-                                 _on(work, torch.uint8, dev, "work"), work.numel(), handle), "qspec_attn_prefix")
+        work = _prompt_workspace(_prompt_workspace_size(dev, n, b, h_q, h_kv), dev, handle)
+    q_p, ld_q = _rows(q, _BF16, dev, n, cols, "q")
+    out_p, ld_out = _rows(out, _BF16, dev, n, cols, "out")
+    args = _PREFIX_ARGS.pack(q_p, ld_q, n, b, cu_p, h_q, h_kv, HEAD_DIM, lens_p, offset, kc, vc, l_max,
+                             _on(prefix_k, _BF16, dev, "prefix_k"), _on(prefix_v, _BF16, dev, "prefix_v"),
+                             prefix_k.shape[1], _one(prefix_len, dev), out_p, ld_out,
+                             _on(work, torch.uint8, dev, "work"), work.numel())
+    _check(LIB.qspec_call(2, args, 21, handle), "qspec_attn_prefix")
     return out

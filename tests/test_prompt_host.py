@@ -101,6 +101,26 @@ def test_prefix_rejects(lib, kw):
     assert _prefix(lib, **kw) == 1
 
 
+def test_call_with_packed_arguments_rejects(lib):
+    """qspec_call: the number of arguments, integers that do not fit, and what the calls themselves refuse."""
+    q = lib._PREFILL_ARGS
+    good = [0x10000, 512, 6, 2, 0x10000, 4, 2, 128, 0x10000, 0x10000, 0x10000, 8, 0x10000000000, 512, 0x10000, 1 << 40]
+    call = lambda op, args, n, fmt=q: lib.LIB.qspec_call(op, fmt.pack(*args), n, None)      # noqa: E731
+    assert lib.LIB.qspec_call(1, None, 16, None) == 1
+    for op, n in ((0, 16), (1, 15), (1, 21), (2, 16), (3, 16), (-1, 16)):
+        assert call(op, good, n) == 1
+    for at, value in ((3, 1 << 31), (3, 0), (5, 1 << 32), (7, 64), (11, -(1 << 40)), (13, 500), (15, -1), (0, 0)):
+        bad = list(good)
+        bad[at] = value
+        assert call(1, bad, 16) == 1
+    rope = [0x10000, 1024, 6, 2, 0, 4, 2, 128, 0, 0, 1e-6, 0x10000, 10, 128, 0, 0x10000, 0, 0x10000, 0x10000, 8,
+            0x10000000000, 512, 0, 0, 0]
+    for at, value in ((10, -1.0), (22, 4), (22, 1 << 32), (22, -1), (24, -1), (13, 12), (16, -1)):
+        bad = list(rope)
+        bad[at] = value
+        assert call(0, bad, 25, lib._ROPE_ARGS) == 1
+
+
 def test_workspace_sizes_refuse_bad_shapes(lib):
     for n, b, h, kv in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 65536, 1, 1), (1, 1, 0, 1), (2 ** 31, 1, 1, 1), (2 ** 30, 1, 64, 8),
                         (1, 1, 4, 0), (1, 1, 4, 3), (1, 1, 129, 1)):
