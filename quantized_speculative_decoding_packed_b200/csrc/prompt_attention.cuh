@@ -18,12 +18,19 @@
 //   warp 9: tcgen05.mma: S of the next step before P V of the current one;
 //   warps 0-3, 4-7: the softmax of slots 0 and 1, a thread for each row.  A slot
 //           is a tile of S, and of O, in tensor memory; P takes S's place;
-//   warps 12-15: the output of an item, while the softmax is at the next.
+//   warps 12-15: the output of an item, while the softmax is at the next;
 //   warp 11: clears the rows of sequences that are refused.
 // With two row tiles, each has a slot, and both use every key tile.  With one,
 // the slots take alternate key tiles and are joined at the end of the item.
 // A piece of a split item is left in the workspace as (m, l, O); a second
 // kernel joins the pieces in order.
+//
+// What bounds it.  Long prompts (8192 tokens, 32 heads over 8: 0.49-0.55 ms, 1.0-1.1 PFLOP/s, at 990 W with the
+// clock at 1.65 GHz): a slot's chain of S (515 cycles), softmax (1600), P V (515) and their hand-overs, about
+// 3300 cycles for a key tile of which the tensor cores work 2060 for both slots.  Single tokens: HBM,
+// and the same chain.  Short prompts: the way to the first item (about 4 us) and HBM's answer to all CTAs'
+// first loads.  Measured and not kept, being slower or no faster: two threads for each row, one pass over S with
+// the maximum kept as a whole number, a third query tile, a fifth key tile, joining in this kernel.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,8 +51,11 @@ constexpr int kPaTileBytes = 128 * kHeadDim * 2;             // 32 KB: a tile of
 constexpr float kScoreLog2 = kInvSqrtHeadDim * 1.4426950408889634f;   // scores in powers of two
 constexpr float kRaise = 8.f;
 
-// How a shared prefix is taken.
+// How a shared prefix is taken: once for the rows of all sequences together, or ahead of the own keys of each.
 enum : int { kPaNoPrefix = 0, kPaPrefixOnce = 1, kPaPrefixAhead = 2 };
+// With so many rows of a KV head in a sequence, on average, the prefix goes ahead of its own keys: 24
+// sequences of 96 rows behind 3000 positions, 64 query heads over 8, 61 us (once for all: 64), of 256 rows 94
+// (139); of 64 rows 60 (52), of 32 rows 57 (41).
 constexpr int kPaAheadRows = 96;
 
 struct PromptArgs {
@@ -58,7 +68,7 @@ struct PromptArgs {
   int64_t off_owners, off_desc, off_ml, off_o, off_row_ml, off_row_o;
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
   int ctas;                    // of the attention's grid
-  int parts;                   // > 0: few items, each has so many CTAs of its own (grid: parts x items)
+  int parts;                   // > 0: few items (and batch <= 32), each can have so many CTAs of its own
 };
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
@@ -185,12 +195,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return d;
 }
-// Two fp32 values rounded to bf16 (nearest even), `lo` in the low half.
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float d;
@@ -291,9 +295,6 @@ struct PaItem {
   int32_t flags, first_cta;
 };
 enum : int { kPaTwo = 1, kPaWhole = 2, kPaCarried = 4, kPaEnds = 8, kPaOnce = 16 };
-
-// The CTA's number.
-__device__ __forceinline__ int pa_cta() { return blockIdx.y * gridDim.x + blockIdx.x; }
 
 struct PaShare {
   int64_t s0, s1, total;
@@ -410,19 +411,26 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
 }
 
 // ---------------------------------------------------------------- the roles of the warps
-// Few items (at most 32 sequences): item blockIdx.y of them in their order, or one of its parts; false
-// where there are not so many.  A part has four key tiles at least.
-__device__ __forceinline__ bool pa_find_one(const PromptArgs& a, PaItem* it) {
+// Few and short items (at most 32 sequences): each has a.parts CTAs of its own, and this one's item, or part
+// of one (four key tiles at least), is found without the shares.  0: there is none for this CTA; -1: the
+// longest item would keep its CTAs for more than kPaPartTiles tiles, so that the shares are better.
+constexpr int kPaPartTiles = 8;
+__device__ __forceinline__ int pa_find_one(const PromptArgs& a, PaItem* it) {
   const int lane = threadIdx.x & 31;
   const int prefix = pa_prefix(a);
   PaSequence mine;
   mine.n = 0;
+  mine.base = 0;
   if (lane < a.batch) mine = pa_sequence(a, lane);
   Run run = pa_prefix_run(a, prefix);
-  int k = blockIdx.y, b = -1, tok0 = 0, items = run_items(run);
+  const Run own = pa_own_run(a, mine, prefix);
+  const int longest = max(run.n > 0 ? run.pre : 0,
+                          __reduce_max_sync(0xffffffffu, own.n > 0 ? item_tiles(own, 0, own.n) : 0));
+  if (longest > kPaPartTiles * a.parts) return -1;
+  int k = blockIdx.x / a.parts, b = -1, tok0 = 0, items = run_items(run);
+  const int part = blockIdx.x - k * a.parts;
   if (k >= items * a.h_kv) {
     k -= items * a.h_kv;
-    const Run own = pa_own_run(a, mine, prefix);
     const int each = run_items(own), all = each * a.h_kv;
     int incl = all;
 #pragma unroll
@@ -431,7 +439,7 @@ __device__ __forceinline__ bool pa_find_one(const PromptArgs& a, PaItem* it) {
       if (lane >= off) incl += o;
     }
     const uint32_t after = __ballot_sync(0xffffffffu, k < incl);
-    if (after == 0) return false;
+    if (after == 0) return 0;
     b = __ffs(after) - 1;
     k -= __shfl_sync(0xffffffffu, incl - all, b);
     items = __shfl_sync(0xffffffffu, each, b);
@@ -442,8 +450,8 @@ __device__ __forceinline__ bool pa_find_one(const PromptArgs& a, PaItem* it) {
   }
   const int g = items == 1 ? k : k / items, i = items == 1 ? 0 : k - g * items;
   const int tokens = item_tokens(run, i), n = item_tiles(run, i, tokens), w = tokens > run.tpt ? 2 : 1;
-  const int parts = min(a.parts, (n + 3) >> 2), part = blockIdx.x;
-  if (part >= parts) return false;
+  const int parts = min(a.parts, (n + 3) >> 2);
+  if (part >= parts) return 0;
   const int first = i * 2 * run.tpt;
   it->tok = tok0 + first;
   it->tokens = tokens;
@@ -457,12 +465,12 @@ __device__ __forceinline__ bool pa_find_one(const PromptArgs& a, PaItem* it) {
   it->sees = run.base + first + 1;
   it->flags = (w == 2 ? kPaTwo : 0) | (parts == 1 ? kPaWhole : 0) | (part > 0 ? kPaCarried : 0) |
               (part == parts - 1 ? kPaEnds : 0) | (b < 0 ? kPaOnce : 0);
-  it->first_cta = pa_cta() - part;
+  it->first_cta = static_cast<int>(blockIdx.x) - part;
   if (a.mode == kPaPrefixOnce && part == 0 && lane == 0) {
     const int64_t at = (b < 0 ? 0 : static_cast<int64_t>(a.n_tok) * a.h_kv) + static_cast<int64_t>(it->tok) * a.h_kv + g;
     reinterpret_cast<int2*>(a.work + a.off_owners)[at] = make_int2(it->first_cta, it->first_cta + parts - 1);
   }
-  return true;
+  return 1;
 }
 
 // Passes an item on (its number `count` in the CTA).
@@ -483,12 +491,14 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   if (a.parts > 0) {
     PaItem one;
-    const bool there = pa_find_one(a, &one);
-    __syncthreads();             // the barriers are there (the other warps have waited for this one)
-    if (there) pa_pass(sm, one, 0, status);
-    one.tokens = 0;
-    pa_pass(sm, one, there ? 1 : 0, status);
-    return;
+    const int there = pa_find_one(a, &one);
+    if (there >= 0) {
+      __syncthreads();           // the barriers are there (the other warps have waited for this one)
+      if (there) pa_pass(sm, one, 0, status);
+      one.tokens = 0;
+      pa_pass(sm, one, there, status);
+      return;
+    }
   }
   const int prefix = pa_prefix(a);
   const Run prefix_run = pa_prefix_run(a, prefix);
@@ -1156,7 +1166,7 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
     items1 += has1;
     if (!(item.flags & kPaWhole) && (item.flags & kPaEnds) && threadIdx.x == kPaThreads - 128) {
       // the item's last piece is here: what the joining kernel has to know
-      PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + pa_cta();
+      PaJoin* const join = reinterpret_cast<PaJoin*>(a.work + a.off_desc) + static_cast<int>(blockIdx.x);
       join->first = item.first_cta;
       join->tok = item.tok;
       join->tokens = item.tokens;
@@ -1204,7 +1214,7 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
       } else {
         float2* ml;
         if (!whole) {                                                 // a piece: columns in blocks of 4
-          const int64_t tile = (static_cast<int64_t>(pa_cta()) * 2 + (item.flags & kPaCarried ? 0 : 1)) * 2 + x;
+          const int64_t tile = (static_cast<int64_t>(static_cast<int>(blockIdx.x)) * 2 + (item.flags & kPaCarried ? 0 : 1)) * 2 + x;
           ml = reinterpret_cast<float2*>(a.work + a.off_ml) + tile * 128 + row;
           dst = reinterpret_cast<float*>(a.work + a.off_o) + tile * 128 * kHeadDim + row * 4;
         } else {
@@ -1270,8 +1280,8 @@ __device__ __forceinline__ void pa_refuse(const PromptArgs& a) {
   const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   const bool no_prefix = pa_prefix(a) < 0;
-  if (no_prefix && pa_cta() == 0 && lane == 0) atomicOr(status, kDevBadInput);
-  for (int b = pa_cta(); b < a.batch; b += gridDim.x * gridDim.y) {
+  if (no_prefix && static_cast<int>(blockIdx.x) == 0 && lane == 0) atomicOr(status, kDevBadInput);
+  for (int b = static_cast<int>(blockIdx.x); b < a.batch; b += gridDim.x) {
     const PaSequence s = pa_sequence(a, b);
     if (!s.bad && !no_prefix) continue;
     if (s.bad && lane == 0) atomicOr(status, kDevBadInput);
@@ -1328,9 +1338,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // Nothing of this call is read or written before the kernels ahead of it are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + pa_cta())->valid = 0;
+  if (tid == 0) (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + static_cast<int>(blockIdx.x))->valid = 0;
   tc_fence_before();
-  if (a.batch > kPaWarpBatch && a.parts == 0) {
+  if (a.batch > kPaWarpBatch) {
     __syncthreads();
     pa_find_share(a, sm);
   } else if (warp != 10) {

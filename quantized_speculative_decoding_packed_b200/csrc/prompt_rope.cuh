@@ -11,10 +11,10 @@
 // column.  A warp owns a head row (a lane holds 4 consecutive columns, one
 // 512-byte load per row), so the norm is one shuffle reduction and the
 // partner column of a split pair comes from another lane at the same
-// place within its four; up to kRopeHeads rows of a warp are in flight.  16300
-// tokens of 80 heads (300 MB): 59.0 us, 5.1 TB/s; with 8 warps a CTA 63.3, with a
-// resident grid that goes through the tokens 85-90 (its warps wait for the small
-// loads in turn, where new CTAs have them under way).
+// place within its four; up to kRopeHeads rows of a warp are in flight.
+// 4900 tokens of 80 heads (302 MB): 57 us, 5.3 TB/s; with
+// a resident grid that goes through the tokens 85-90 (its warps wait for the
+// small loads in turn, where new CTAs have them under way).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,6 +28,13 @@ namespace qspec {
 constexpr int kRopeWarps = 4; 
 constexpr int kRopeHeads = 4;                 // head rows of a warp, loaded together
 constexpr int kRopeHeadsPerCta = kRopeWarps * kRopeHeads;
+
+// Two fp32 values rounded to bf16 (nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 
 struct RopeArgs {
   const float* qkv;            // no restrict: q_out may be the same rows
@@ -70,7 +77,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const 
   const int tok = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.h_q + 2 * a.h_kv;
-  const float* row = a.qkv + static_cast<int64_t>(tok) * a.ld;
+  const float* row = a.qkv + static_cast<int64_t>(tok) * a.ld + lane * 4;
   const int h0 = blockIdx.y * kRopeHeadsPerCta + warp;
   // the rows first: what follows is a chain of small loads
   float x[kRopeHeads][4];
@@ -78,7 +85,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const 
   for (int u = 0; u < kRopeHeads; ++u) {
     const int h = h0 + u * kRopeWarps;
     if (h < heads) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(row + static_cast<int64_t>(h) * kHeadDim + lane * 4));
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(row + h * kHeadDim));
       x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
     }
   }
@@ -133,6 +140,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const 
       sn[0] = sg * s.x; sn[1] = sg * s.y; sn[2] = sg * s.z; sn[3] = sg * s.w;
     }
   }
+  const int64_t q_at = static_cast<int64_t>(tok) * a.ld_q + lane * 4;
+  const int64_t kv_at = (static_cast<int64_t>(b) * a.h_kv * a.l_max + pos) * kHeadDim + lane * 4;
 #pragma unroll
   for (int u = 0; u < kRopeHeads; ++u) {
     const int h = h0 + u * kRopeWarps;
@@ -169,18 +178,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const 
       }
     }
     if (h < a.h_q) {
-      const int64_t at = static_cast<int64_t>(tok) * a.ld_q + static_cast<int64_t>(h) * kHeadDim + lane * 4;
       if (a.q_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + at) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + q_at + h * kHeadDim) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
       else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.q_out) + at) =
-            make_uint2(pack_bf16x2(x[u][0], x[u][1]), pack_bf16x2(x[u][2], x[u][3]));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.q_out) + q_at + h * kHeadDim) =
+            make_uint2(cvt_bf16x2(x[u][0], x[u][1]), cvt_bf16x2(x[u][2], x[u][3]));
     } else {
       const int g = h - a.h_q - (is_v ? a.h_kv : 0);
       uint16_t* cache = is_v ? a.v_cache : a.k_cache;
-      const int64_t at = ((static_cast<int64_t>(b) * a.h_kv + g) * a.l_max + pos) * kHeadDim + lane * 4;
-      *reinterpret_cast<uint2*>(cache + at) =
-          make_uint2(pack_bf16x2(x[u][0], x[u][1]), pack_bf16x2(x[u][2], x[u][3]));
+      *reinterpret_cast<uint2*>(cache + kv_at + static_cast<int64_t>(g) * a.l_max * kHeadDim) =
+          make_uint2(cvt_bf16x2(x[u][0], x[u][1]), cvt_bf16x2(x[u][2], x[u][3]));
     }
   }
 }

@@ -499,16 +499,16 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.l_max = l_max;
   a.prefix_max = with_prefix ? prefix_max : 0;
   a.mode = mode;
-  // Few items (by what the host knows: at most so many, of at most so many key tiles): a CTA takes one, or
-  // a part of one, which it finds at once.  Else the shares of prompt_schedule.cuh.  (Measured for one
-  // prompt of 200 tokens, 32 heads over 8: 13.3 us against 19.4.)
+  // Few items, by what the host knows (at most so many): where they are short too, a CTA takes one, or a part
+  // of one, which it finds at once, else its share.  (One prompt of 200 tokens, 32 heads over 8: 13.3 us,
+  // by shares 19.4.)
   const int64_t runs = (n_tok + 2 * a.tpt - 1) / (2 * a.tpt);
   const int64_t items = h_kv * (runs + (cu || batch > 1 ? batch : 0) + (a.mode == kPaPrefixOnce ? runs : 0));
-  const int64_t most_tiles = (static_cast<int64_t>(l_max) + 127) / 128 + (with_prefix ? (static_cast<int64_t>(prefix_max) + 127) / 128 : 0);
   a.parts = batch <= 32 && items <= grid ? static_cast<int>(grid / items) : 0;
-  if (a.parts > (most_tiles + 3) / 4) a.parts = static_cast<int>((most_tiles + 3) / 4);
-  const dim3 shape = a.parts > 0 ? dim3(static_cast<unsigned>(a.parts), static_cast<unsigned>(items)) : dim3(static_cast<unsigned>(grid));
-  a.ctas = static_cast<int>(shape.x * shape.y);
+  // no item can be split: one CTA each, by the capacity of the caches
+  const int64_t most_tiles = (static_cast<int64_t>(l_max) + 127) / 128 + (with_prefix ? (static_cast<int64_t>(prefix_max) + 127) / 128 : 0);
+  const bool unsplit = a.parts > 0 && (most_tiles <= 4 || (a.parts == 1 && most_tiles <= kPaPartTiles));
+  a.ctas = grid;
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
   const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};
@@ -521,11 +521,11 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   tpv = tv;
   if (with_prefix && (!make_kv_tmap(&tpk, prefix_k, h_kv, prefix_max) || !make_kv_tmap(&tpv, prefix_v, h_kv, prefix_max)))
     return QSPEC_ERR_CUDA;
-  st = launch_dependent(prompt_attention_kernel, shape, kPaThreads, kPaSmemBytes, stream,
+  st = launch_dependent(prompt_attention_kernel, dim3(static_cast<unsigned>(grid)), kPaThreads, kPaSmemBytes, stream,
                         tq, tk, tv, tpk, tpv, a);
   if (st != QSPEC_OK) return st;
-  if (a.mode != kPaPrefixOnce && a.parts == 1) return QSPEC_OK;          // no item is split
-  if (a.mode != kPaPrefixOnce) return launch_dependent(prompt_join_kernel, dim3(shape.x * shape.y, 8), 256, 0, stream, a);
+  if (a.mode != kPaPrefixOnce && unsplit) return QSPEC_OK;
+  if (a.mode != kPaPrefixOnce) return launch_dependent(prompt_join_kernel, dim3(static_cast<unsigned>(grid), 8), 256, 0, stream, a);
   return launch_dependent(prefix_join_kernel, dim3(static_cast<unsigned>((n_tok * h_q + 7) / 8)), 256, 0, stream, a);
 }
 

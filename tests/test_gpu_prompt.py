@@ -7,7 +7,9 @@ A = max_j sum_i |q_i k_ji| / sqrt(128) of its row:
   * a score is a sum of 128 exact products in fp32 (2^-24 each, taken twice, for the tensor
     cores may cut instead of round): an error of 2^-16 A in the exponent, in weight and sum: 2^-15 A W
   * the sum of weights and the weighted values over n keys in fp32:            n 2^-22 W
-  * exp2 (2^-18) and its argument (2^-24 of at most 2^6 for weights that count): 2^-16 W
+  * exp2: a quarter of the weights come from a cubic that is off by up to 7.5e-5, the others from ex2 (2^-22);
+    the argument has 2^-24 of at most 2^6 for weights that count.  In a weight and in the sum of weights
+    that divides it, 2 (7.5e-5 + 2^-18) = 1.58e-4 < 2.44e-4:                    2^-12 W
   * the output rounded to bf16:                                                2^-8 |out|
 The products of these are below 1 % of their sum.
 """
@@ -55,7 +57,7 @@ def _attention64(q, keys, values, hidden):
     out, mag = w @ v, w @ v.abs()
     a = ((q.abs() @ k.abs().T) / math.sqrt(D)).masked_fill(hidden, 0).amax(-1, keepdim=True)
     n = k.shape[0]
-    bound = 1.01 * (2.0 ** -8 * (mag + out.abs()) + mag * (2.0 ** -15 * a + n * 2.0 ** -22 + 2.0 ** -16))
+    bound = 1.01 * (2.0 ** -8 * (mag + out.abs()) + mag * (2.0 ** -15 * a + n * 2.0 ** -22 + 2.0 ** -12))
     return out, bound
 
 
@@ -122,6 +124,8 @@ PREFILL = [
     ([1, 1, 1], [15, 16, 17], 128, 1),
     ([1500], [0], 2, 2),
     ([300, 1, 2000], [1000, 4000, 0], 4, 2),
+    ([1] * 20, [150 * b for b in range(20)], 16, 4),          # few items, too long for one CTA each
+    ([2] * 9, [1000, 0, 3, 800, 127, 128, 129, 500, 1020], 8, 8),     # and short enough
 ]
 
 
@@ -211,6 +215,8 @@ PREFIX = [
     ([700, 5], [0, 9], 2, 1, 900),            # long runs behind a prefix that ends inside a tile
     ([1200], [300], 8, 8, 400),
     (300, [0, 130, 70], 4, 4, 1050),
+    (16, [40] * 8, 8, 2, 5000),               # few items, too long for one CTA each
+    (1, [40] * 30, 4, 4, 900),                # and short enough
 ]
 
 
