@@ -28,7 +28,7 @@
 // What bounds it.  Long prompts (8192 tokens, 32 heads over 8: 0.49-0.55 ms, 1.0-1.1 PFLOP/s, at 990 W with the
 // clock at 1.65 GHz): a slot's chain of S (515 cycles), softmax (1600), P V (515) and their hand-overs, about
 // 3300 cycles for a key tile of which the tensor cores work 2060 for both slots.  Single tokens: HBM,
-// and the same chain.  Short prompts: the way to the first item (about 4 us) and HBM's answer to all CTAs'
+// and the same chain.  Short prompts: the way to the first item (about 5 us) and HBM's answer to all CTAs'
 // first loads.  Measured and not kept, being slower or no faster: two threads for each row, one pass over S with
 // the maximum kept as a whole number, a third query tile, a fifth key tile, joining in this kernel.
 #pragma once
