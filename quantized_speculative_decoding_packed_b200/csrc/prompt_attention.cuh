@@ -412,9 +412,13 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
 
 // ---------------------------------------------------------------- the roles of the warps
 // Few and short items (at most 32 sequences): each has a.parts CTAs of its own, and this one's item, or part
-// of one (four key tiles at least), is found without the shares.  0: there is none for this CTA; -1: the
+// of one (kPaMinPart key tiles at least), is found without the shares.  0: there is none for this CTA; -1: the
 // longest item would keep its CTAs for more than kPaPartTiles tiles, so that the shares are better.
+// us with 4, 6, 8, 12, 16 tiles at most (16 x 1 token behind 1000, 32 heads over 8): 26 26 21 21 21;
+// 3 x 20 behind 4000, 64 over 8: 31 31 31 37 37.  With parts of 4, 3, 2 tiles at least: 64 tokens behind
+// 1000 20.0 20.1 18.9, 4 x 1 behind a prefix of 500 15.7 13.9 13.9.
 constexpr int kPaPartTiles = 8;
+constexpr int kPaMinPart = 2;
 __device__ __forceinline__ int pa_find_one(const PromptArgs& a, PaItem* it) {
   const int lane = threadIdx.x & 31;
   const int prefix = pa_prefix(a);
@@ -450,7 +454,7 @@ __device__ __forceinline__ int pa_find_one(const PromptArgs& a, PaItem* it) {
   }
   const int g = items == 1 ? k : k / items, i = items == 1 ? 0 : k - g * items;
   const int tokens = item_tokens(run, i), n = item_tiles(run, i, tokens), w = tokens > run.tpt ? 2 : 1;
-  const int parts = min(a.parts, (n + 3) >> 2);
+  const int parts = min(a.parts, (n + kPaMinPart - 1) / kPaMinPart);
   if (part >= parts) return 0;
   const int first = i * 2 * run.tpt;
   it->tok = tok0 + first;

@@ -25,7 +25,7 @@
 
 namespace qspec {
 
-constexpr int kRopeWarps = 4; 
+constexpr int kRopeWarps = 4;
 constexpr int kRopeHeads = 4;                 // head rows of a warp, loaded together
 constexpr int kRopeHeadsPerCta = kRopeWarps * kRopeHeads;
 

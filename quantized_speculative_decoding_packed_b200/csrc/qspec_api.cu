@@ -507,7 +507,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   a.parts = batch <= 32 && items <= grid ? static_cast<int>(grid / items) : 0;
   // no item can be split: one CTA each, by the capacity of the caches
   const int64_t most_tiles = (static_cast<int64_t>(l_max) + 127) / 128 + (with_prefix ? (static_cast<int64_t>(prefix_max) + 127) / 128 : 0);
-  const bool unsplit = a.parts > 0 && (most_tiles <= 4 || (a.parts == 1 && most_tiles <= kPaPartTiles));
+  const bool unsplit = a.parts > 0 && (most_tiles <= kPaMinPart || (a.parts == 1 && most_tiles <= kPaPartTiles));
   a.ctas = grid;
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
