@@ -495,10 +495,9 @@ _PROMPT_WS: dict = {}
 _PROMPT_WS_RETIRED: list = []
 
 
-def _new_prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-        ws[:PROMPT_WORKSPACE_ZERO].zero_()
+def _new_prompt_workspace(nbytes: int, dev: int) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    ws[:PROMPT_WORKSPACE_ZERO].zero_()
     return ws
 
 
@@ -516,16 +515,18 @@ def prompt_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
 
 
 def _prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
+    if handle != _raw_stream(dev):
+        # the stream that will use it decides whether a graph is captured, and when the memory is free again
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+            return _prompt_workspace(nbytes, dev, handle)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-        ws[:PROMPT_WORKSPACE_ZERO].zero_()
-        return ws
+        return _new_prompt_workspace(nbytes, dev)
     cur = _PROMPT_WS.get((dev, handle))
     if cur is None or cur.numel() < nbytes:
         if cur is not None:
             _PROMPT_WS_RETIRED.append(cur)
             nbytes = max(nbytes, 2 * cur.numel())
-        cur = _new_prompt_workspace(nbytes, dev, handle)
+        cur = _new_prompt_workspace(nbytes, dev)
         _PROMPT_WS[(dev, handle)] = cur
     return cur
 

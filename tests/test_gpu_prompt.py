@@ -475,6 +475,29 @@ def test_two_streams_and_graphs(qs):
         assert all(torch.equal(x, y) for x, y in zip(eager, want[i]))
 
 
+def test_captured_call_on_a_forked_stream_has_its_own_workspace(qs):
+    """stream= names another stream than the captured one that is current: two calls at once in a graph."""
+    new, old, h_q, h_kv = [300, 20], [500, 900], 8, 2
+    runs = [_case(seed, new, old, h_q, h_kv) for seed in (41, 42)]
+    outs = [torch.empty(sum(new), h_q * D, dtype=torch.bfloat16, device="cuda") for _ in runs]
+    want = [qs.attn_prefill(q, cu, lens, kc, vc, h_q) for q, kc, vc, cu, lens in runs]
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        for (q, kc, vc, cu, lens), out, stream in zip(runs, outs, (side, None)):
+            qs.attn_prefill(q, cu, lens, kc, vc, h_q, out=out, stream=stream)
+        main.wait_stream(side)
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for out, ref in zip(outs, want):
+            assert torch.equal(out, ref)
+
+
 def test_default_workspace_grows_and_is_kept(qs):
     """A larger call after a captured one: the graph's own buffer is untouched, the eager one is replaced."""
     h_q, h_kv, plen = 4, 2, 100
