@@ -405,8 +405,9 @@ qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_token
 
 /* Attention of a batch whose sequences share one prefix: token t of sequence b
  * sees the *prefix_len positions of the prefix and positions 0 .. lens[b] + offset + t
- * of its own cache, under one softmax.  The prefix is read once for the tokens of
- * all sequences together.
+ * of its own cache, under one softmax.  The prefix is taken once for the tokens of
+ * all sequences together; where these fill tiles of 128 rows by themselves (about 96
+ * query rows a KV head and sequence), ahead of each sequence's own keys.
  *  prefix_k, prefix_v  bf16 [h_kv][prefix_max][128] (a cache of batch 1, filled like any other).
  *  prefix_len  device int32 [1], 0 .. prefix_max; otherwise every output row is zero and
  *              QSPEC_ERR_BAD_INPUT is reported.
