@@ -372,8 +372,8 @@ qspec_status qspec_rope_table(const double* inv_freq, int32_t rot, int64_t posit
  *  table      as qspec_rope_table writes it, `positions` rows; rot = 0: no rotation (table NULL).
  *  prefix_len device int32 [1] or NULL (0): tokens of a shared prefix before every sequence.
  *  q_out      the queries: bf16 [n_tokens][ld_q], or fp32 with QSPEC_ROPE_Q_FP32.  fp32 queries may be
- *             turned in place (q_out = qkv, ld_q = ld_qkv): the rows are then what qspec_attn_decode
- *             takes.  No other overlap.
+ *             turned in place (q_out = qkv, and ld_q = ld_qkv unless there is one token): the rows are
+ *             then what qspec_attn_decode takes.  No other overlap.
  *  workspace  optional (NULL, or >= 256 zeroed bytes): the status word.  A token whose position is
  *             outside the cache or the table writes nothing and is reported there.
  * Requires rot a multiple of 8 in [0, 128], ld_qkv >= (h_q + 2 h_kv) * 128 and a multiple of 4,

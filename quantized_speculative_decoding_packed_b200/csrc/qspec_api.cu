@@ -868,8 +868,9 @@ qspec_status qspec_qkv_rope_append(const float* qkv, int64_t ld_qkv, int64_t n_t
       !aligned(k_gamma, 16) || !aligned(table, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(q_out, 16))
     return QSPEC_ERR_INVALID_ARG;
-  // the queries may be turned in place, nothing else of the projection may be written over
-  const bool in_place = q32 && q_out == qkv && ld_q == ld_qkv;
+  // the queries may be turned in place, nothing else of the projection may be written over (the row
+  // strides say nothing where there is one row)
+  const bool in_place = q32 && q_out == qkv && (n_tokens == 1 || ld_q == ld_qkv);
   if (!in_place &&
       overlap(qkv, ((n_tokens - 1) * ld_qkv + all) * 4, q_out, ((n_tokens - 1) * ld_q + cols) * (q32 ? 4 : 2)))
     return QSPEC_ERR_INVALID_ARG;

@@ -472,7 +472,8 @@ def _rows(t: torch.Tensor, dtype, dev: int, rows: int, columns: int, name: str):
     if len(shape) != 2 or shape[0] != rows or shape[1] < columns:
         raise ValueError(f"{name} must be [{rows}][{columns}], not {list(shape)}")
     if t.is_contiguous():
-        return t.data_ptr(), shape[1]
+        # one row has no stride of its own: a slice of a wider one counts as contiguous
+        return t.data_ptr(), shape[1] if rows > 1 else columns
     ld, step = t.stride()
     if step != 1:
         raise ValueError(f"{name} must have unit column stride")
