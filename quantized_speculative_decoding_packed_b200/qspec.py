@@ -5,7 +5,10 @@ kernels of the library.  Importing this module loads the library and raises
 if it is missing; there is no fallback implementation.
 
 Functions take CUDA torch tensors (contiguous, on the current device) and
-launch on the current torch stream unless `stream` is given.
+launch on the current torch stream unless `stream` is given.  Outputs that are
+not given are memory of the stream that the call runs on; the caller orders
+the streams (inputs ready before, outputs read after) and keeps the inputs
+until the call is done, as with any torch operation on another stream.
 """
 from __future__ import annotations
 
@@ -123,6 +126,20 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """An output that is not given: memory of the stream that writes it.
+
+    A block that the current stream has freed may still be in use by work queued there, for which
+    another stream does not wait; and this one is kept until the current stream is done with it too.
+    """
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _need(t: torch.Tensor, dtype, name: str) -> None:
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
@@ -168,9 +185,9 @@ def quantize_weights(w: torch.Tensor, group: int = 128, wq: torch.Tensor | None 
     _need(w, torch.float32, "w")
     n, k = w.shape
     if wq is None:
-        wq = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+        wq = _empty(stream, (n, k // 2), torch.uint8, w.device)
     if ws is None:
-        ws = torch.empty((n, scale_row_stride(k, group)), dtype=torch.float16, device=w.device)
+        ws = _empty(stream, (n, scale_row_stride(k, group)), torch.float16, w.device)
     _check(LIB.qspec_quantize_weights(_ptr(w), n, k, group, _ptr(wq), _ptr(ws), _stream(stream)),
            "qspec_quantize_weights")
     return wq, ws
@@ -182,9 +199,9 @@ def quant_act(x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tensor 
     _need(x, torch.bfloat16, "x")
     m, k = x.shape
     if xq is None:
-        xq = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+        xq = _empty(stream, (m, k // 2), torch.uint8, x.device)
     if xs is None:
-        xs = torch.empty((m,), dtype=torch.float32, device=x.device)
+        xs = _empty(stream, (m,), torch.float32, x.device)
     _check(LIB.qspec_quant_act(_ptr(x), m, k, _ptr(xq), _ptr(xs), _stream(stream)),
            "qspec_quant_act")
     return xq, xs
@@ -201,7 +218,7 @@ def cast_bf16(y: torch.Tensor, k: int | None = None, x: torch.Tensor | None = No
     m, n = y.shape
     k = n if k is None else k
     if x is None:
-        x = torch.empty((m, k), dtype=torch.bfloat16, device=y.device)
+        x = _empty(stream, (m, k), torch.bfloat16, y.device)
     _check(LIB.qspec_cast_bf16(_ptr(y), m, n, k, _ptr(x), _stream(stream)), "qspec_cast_bf16")
     return x
 
@@ -259,7 +276,7 @@ def _drafting(mode, x, wq, ws, group, y, work, dbg_acc, stream, weights_ready, f
     n = wq.shape[0]
     op = OP_GEMM_W4A4 if mode == "w4a4" else OP_GEMM_W4A8
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (m, n), torch.float32, x.device)
     need = workspace_size(op, m, n, k, group)
     if work is None:
         work = workspace(need, x.device)
@@ -286,7 +303,7 @@ def gemm_w4a16(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, group: int =
     m, k = x.shape
     n = wq.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (m, n), torch.float32, x.device)
     need = workspace_size(OP_GEMM_W4A16, m, n, k, group)
     if work is None:
         work = workspace(need, x.device)
@@ -308,7 +325,7 @@ def gemm_w4a16_noalloc(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, grou
     m, k = x.shape
     n = wq.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (m, n), torch.float32, x.device)
     _check(LIB.qspec_gemm_w4a16_noalloc(_ptr(x), m, k, _ptr(wq), _ptr(ws), n, group, _ptr(y),
                                         GEMM_WEIGHTS_READY if weights_ready else 0,
                                         _stream(stream)), "qspec_gemm_w4a16_noalloc")
@@ -333,9 +350,9 @@ def spec_accept(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_acc: to
     b, g1, v = p.shape
     gamma = g1 - 1
     if n_accepted is None:
-        n_accepted = torch.empty((b,), dtype=torch.int32, device=p.device)
+        n_accepted = _empty(stream, (b,), torch.int32, p.device)
     if tokens is None:
-        tokens = torch.empty((b, gamma + 1), dtype=torch.int32, device=p.device)
+        tokens = _empty(stream, (b, gamma + 1), torch.int32, p.device)
     nbytes = 0 if work is None else work.numel()
     _check(LIB.qspec_spec_accept(_ptr(p), _ptr(q), _ptr(draft), _ptr(u_acc), _ptr(u_res), b, gamma,
                                  v, _ptr(n_accepted), _ptr(tokens), _ptr(work), nbytes,
@@ -352,9 +369,9 @@ def spec_accept_greedy(p: torch.Tensor, draft: torch.Tensor, n_accepted: torch.T
     b, g1, v = p.shape
     gamma = g1 - 1
     if n_accepted is None:
-        n_accepted = torch.empty((b,), dtype=torch.int32, device=p.device)
+        n_accepted = _empty(stream, (b,), torch.int32, p.device)
     if tokens is None:
-        tokens = torch.empty((b, gamma + 1), dtype=torch.int32, device=p.device)
+        tokens = _empty(stream, (b, gamma + 1), torch.int32, p.device)
     nbytes = 0 if work is None else work.numel()
     _check(LIB.qspec_spec_accept_greedy(_ptr(p), _ptr(draft), b, gamma, v, _ptr(n_accepted),
                                         _ptr(tokens), _ptr(work), nbytes, _stream(stream)),
@@ -425,7 +442,7 @@ def attn_decode(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: tor
     b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)
     t_new = _tokens_per_sequence(qkv, b)
     if out is None:
-        out = torch.empty((b * t_new, h_q * HEAD_DIM), dtype=torch.float32, device=qkv.device)
+        out = _empty(stream, (b * t_new, h_q * HEAD_DIM), torch.float32, qkv.device)
     if work is None:
         work = _attn_workspace(attn_workspace_size(b, t_new, h_q, h_kv, ctx_max), qkv.device, b * h_kv)
     _check(LIB.qspec_attn_decode(_ptr(qkv), qkv.stride(0), b, t_new, h_q, h_kv, HEAD_DIM,
@@ -583,7 +600,7 @@ def rope_table(inv_freq: torch.Tensor, positions: int, table: torch.Tensor | Non
     rot = 2 * inv_freq.numel()
     freq = _on(inv_freq, torch.float64, dev, "inv_freq")
     if table is None:
-        table = torch.empty((positions, rot), dtype=_F32, device=inv_freq.device)
+        table = _empty(stream, (positions, rot), _F32, inv_freq.device)
     if tuple(table.shape) != (positions, rot):
         raise ValueError(f"table must be [{positions}][{rot}]")
     _check(LIB.qspec_rope_table(freq, rot, positions, _on(table, _F32, dev, "table"),
@@ -620,7 +637,7 @@ def qkv_rope_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache:
                 raise ValueError(f"q_gamma and k_gamma must have {HEAD_DIM} entries")
             gammas[i] = _on(gamma, _F32, dev, "q_gamma" if i == 0 else "k_gamma")
     if q_out is None:
-        q_out = torch.empty((n, h_q * HEAD_DIM), dtype=_BF16, device=qkv.device)
+        q_out = _empty(stream, (n, h_q * HEAD_DIM), _BF16, qkv.device)
     if q_out.dtype is not _BF16 and q_out.dtype is not _F32:
         raise ValueError("q_out must be bf16 or fp32")
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_Q_FP32 if q_out.dtype is _F32 else 0)
@@ -650,7 +667,7 @@ def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache:
     n, cols = q.shape[0], h_q * HEAD_DIM
     lens_p, cu_p = _packed_on(cu, lens, b, n, dev)
     if out is None:
-        out = torch.empty((n, cols), dtype=_BF16, device=q.device)
+        out = _empty(stream, (n, cols), _BF16, q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
         work = _prompt_workspace(_prompt_workspace_size(dev), dev, handle)
@@ -679,7 +696,7 @@ def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
     if prefix_k.dim() != 3 or prefix_k.shape != prefix_v.shape or prefix_k.shape[0] != h_kv or prefix_k.shape[2] != HEAD_DIM:
         raise ValueError(f"prefix_k and prefix_v must both be [{h_kv}][positions][{HEAD_DIM}]")
     if out is None:
-        out = torch.empty((n, cols), dtype=_BF16, device=q.device)
+        out = _empty(stream, (n, cols), _BF16, q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
         work = _prompt_workspace(_prompt_workspace_size(dev, n, b, h_q, h_kv), dev, handle)
