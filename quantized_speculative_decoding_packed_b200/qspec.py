@@ -16,6 +16,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 import torch
 
@@ -37,6 +38,7 @@ EXPORTED = ("qspec_quantize_weights", "qspec_quant_act", "qspec_cast_bf16", "qsp
             "qspec_attn_prefill_workspace_size", "qspec_attn_prefix",
             "qspec_attn_prefix_workspace_size", "qspec_call", "qspec_abi_version")
 ABI_VERSION = 5
+_raw_stream = torch._C._cuda_getCurrentRawStream     # the current stream of a device, as a plain handle
 HEAD_DIM = 128           # the KV-cache calls' head dimension
 ROPE_INTERLEAVED, ROPE_Q_FP32 = 1, 2
 GEMM_WEIGHTS_READY = 1   # flag: wq/ws are not written by work still in flight
@@ -405,18 +407,42 @@ def attn_workspace_size(batch: int, t_new: int, h_q: int, h_kv: int, ctx_max: in
     return int(LIB.qspec_attn_workspace_size(batch, t_new, h_q, h_kv, HEAD_DIM, ctx_max))
 
 
-# attn_decode's default workspaces, by device and number of arrival counters: the partial
-# results behind the counters lie where the GEMMs keep their split-tile tickets, and where
-# a call with more counters has counters, which must both be zero.
-_ATTN_WS_CACHE: dict = {}
+class _StreamBuffers(threading.local):
+    """Default workspaces of one host thread, by device and stream.  Work of two streams may overlap; and what
+    two threads enqueue on one stream may interleave between the kernels of a call."""
+
+    def __init__(self):
+        self.of = {}
 
 
-def _attn_workspace(nbytes: int, device: torch.device, counters: int) -> torch.Tensor:
-    cur = _ATTN_WS_CACHE.get((device, counters))
-    if cur is None or cur.numel() < nbytes:
-        cur = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ATTN_WS_CACHE[(device, counters)] = cur
-    return cur
+# attn_decode's own: [buffer, bytes from its start that are zero between calls].  The partial results lie
+# behind a call's arrival counters, where the GEMMs keep their split-tile tickets, and where a call with
+# more counters has counters; so the buffer is not the GEMMs', and those that a call with fewer counters
+# has written over are cleared before they count again.
+_ATTN_WS = _StreamBuffers()
+
+
+def _attn_workspace(nbytes: int, dev: int, counters: int, stream=None) -> torch.Tensor:
+    if stream is not None:
+        # it decides whether a graph is captured, owns the memory and clears it
+        with torch.cuda.stream(stream):
+            return _attn_workspace(nbytes, dev, counters)
+    handle = _raw_stream(dev)
+    head = 256 + 4 * counters
+    if torch.cuda.is_current_stream_capturing():
+        # the graph's alone, and cleared in it: an eager call could run before the graph, and would outgrow it
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        ws[:head].zero_()
+        return ws
+    cur = _ATTN_WS.of.get((dev, handle))
+    if cur is None or cur[0].numel() < nbytes:
+        cur = [torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}"), 0]
+        _ATTN_WS.of[dev, handle] = cur
+    ws, clear = cur
+    if head > clear:
+        ws[clear:head].zero_()
+    cur[1] = head
+    return ws
 
 
 def kv_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor,
@@ -444,7 +470,10 @@ def attn_decode(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: tor
     if out is None:
         out = _empty(stream, (b * t_new, h_q * HEAD_DIM), torch.float32, qkv.device)
     if work is None:
-        work = _attn_workspace(attn_workspace_size(b, t_new, h_q, h_kv, ctx_max), qkv.device, b * h_kv)
+        need = attn_workspace_size(b, t_new, h_q, h_kv, ctx_max)
+        if need == 0:
+            raise QSpecError(1, "qspec_attn_decode")
+        work = _attn_workspace(need, qkv.get_device(), b * h_kv, stream)
     _check(LIB.qspec_attn_decode(_ptr(qkv), qkv.stride(0), b, t_new, h_q, h_kv, HEAD_DIM,
                                  _ptr(lens), offset, _ptr(k_cache), _ptr(v_cache), l_max, ctx_max,
                                  _ptr(out), out.stride(0), _ptr(work), work.numel(),
@@ -469,7 +498,6 @@ def kv_commit(lens: torch.Tensor, n_accepted: torch.Tensor, l_max: int,
 # object), and the arguments go to the library in one block (qspec_call; 25 arguments of a
 # ctypes call take 3 us).
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream
 _ROPE_ARGS, _PREFILL_ARGS, _PREFIX_ARGS = (struct.Struct(f) for f in ("10qd14q", "16q", "21q"))
 
 
