@@ -534,10 +534,9 @@ def _current_device(t: torch.Tensor) -> int:
     return dev
 
 
-# Default workspaces of the prompt attention, by device and stream: calls on two
-# streams have two.  One that has become too small is kept, for a captured graph may
-# still write to it.
-_PROMPT_WS: dict = {}
+# Default workspaces of the prompt attention.  One that has become too small is kept, for who asked for it
+# may still use it.
+_PROMPT_WS = _StreamBuffers()
 _PROMPT_WS_RETIRED: list = []
 
 
@@ -551,29 +550,32 @@ PROMPT_WORKSPACE_ZERO = 256       # bytes of a prompt attention workspace that s
 
 
 def prompt_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    """A scratch buffer of at least `nbytes` bytes for the prompt attention calls on one stream.
+    """The scratch buffer, of at least `nbytes` bytes, that the prompt attention calls of this thread take
+    where `work` is not given, on one stream: workspace_status of it tells what they have reported.
 
-    Under stream capture the buffer belongs to the graph alone.  Graphs that share a buffer
-    passed as `work` must not run at the same time.
+    Under stream capture the buffer is a new one that belongs to the graph alone; to read the status of
+    captured calls, pass them a buffer as `work`.  Graphs that share one must not run at the same time, and
+    neither must calls of two threads.
     """
     dev = torch.device(device).index if torch.device(device).index is not None else torch.cuda.current_device()
-    return _prompt_workspace(nbytes, dev, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    return _prompt_workspace(nbytes, dev, stream)
 
 
-def _prompt_workspace(nbytes: int, dev: int, handle: int) -> torch.Tensor:
-    if handle != _raw_stream(dev):
-        # the stream that will use it decides whether a graph is captured, and when the memory is free again
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-            return _prompt_workspace(nbytes, dev, handle)
+def _prompt_workspace(nbytes: int, dev: int, stream=None) -> torch.Tensor:
+    if stream is not None:
+        # it decides whether a graph is captured, owns the memory and clears it
+        with torch.cuda.stream(stream):
+            return _prompt_workspace(nbytes, dev)
     if torch.cuda.is_current_stream_capturing():
         return _new_prompt_workspace(nbytes, dev)
-    cur = _PROMPT_WS.get((dev, handle))
+    key = dev, _raw_stream(dev)
+    cur = _PROMPT_WS.of.get(key)
     if cur is None or cur.numel() < nbytes:
         if cur is not None:
             _PROMPT_WS_RETIRED.append(cur)
             nbytes = max(nbytes, 2 * cur.numel())
         cur = _new_prompt_workspace(nbytes, dev)
-        _PROMPT_WS[(dev, handle)] = cur
+        _PROMPT_WS.of[key] = cur
     return cur
 
 
@@ -698,7 +700,7 @@ def attn_prefill(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, k_cache:
         out = _empty(stream, (n, cols), _BF16, q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = _prompt_workspace(_prompt_workspace_size(dev), dev, handle)
+        work = _prompt_workspace(_prompt_workspace_size(dev), dev, stream)
     q_p, ld_q = _rows(q, _BF16, dev, n, cols, "q")
     out_p, ld_out = _rows(out, _BF16, dev, n, cols, "out")
     args = _PREFILL_ARGS.pack(q_p, ld_q, n, b, cu_p, h_q, h_kv, HEAD_DIM, lens_p, kc, vc, l_max, out_p, ld_out,
@@ -727,7 +729,7 @@ def attn_prefix(q: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
         out = _empty(stream, (n, cols), _BF16, q.device)
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if work is None:
-        work = _prompt_workspace(_prompt_workspace_size(dev, n, b, h_q, h_kv), dev, handle)
+        work = _prompt_workspace(_prompt_workspace_size(dev, n, b, h_q, h_kv), dev, stream)
     q_p, ld_q = _rows(q, _BF16, dev, n, cols, "q")
     out_p, ld_out = _rows(out, _BF16, dev, n, cols, "out")
     args = _PREFIX_ARGS.pack(q_p, ld_q, n, b, cu_p, h_q, h_kv, HEAD_DIM, lens_p, offset, kc, vc, l_max,

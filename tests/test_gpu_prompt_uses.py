@@ -1,6 +1,7 @@
 """The prompt path as programs may call it: one token in place, on other streams, from threads, captured, with
 starts that are out of order and values that are not finite."""
 import math
+import threading
 
 import pytest
 import torch
@@ -99,3 +100,116 @@ def test_default_output_is_memory_of_the_named_stream(qs, name):
         fresh = [torch.full_like(want, 9) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(fresh) == 3
+
+
+# ---------------------------------------------------------------- default workspaces
+@pytest.fixture
+def fresh(qs, monkeypatch):
+    """No default workspace from before; the buffers that the test's own thread gets."""
+    buffers = qs._StreamBuffers()
+    monkeypatch.setattr(qs, "_PROMPT_WS", buffers)
+    monkeypatch.setattr(qs, "_PROMPT_WS_RETIRED", [])
+    return buffers
+
+
+def test_threads_on_one_stream(qs, fresh):
+    """Each thread's calls, an attention and a join each, interleave with the others' on the default stream."""
+    plen, h_q, h_kv = 700, 8, 2
+    pk, pv = _prefix(11, h_kv, plen)
+    plen_d = _i32([plen])
+    shapes = [([40, 300, 7], [900, 0, 200]), ([1] * 30, [50] * 30), ([600], [1500]), ([5] * 9, [300] * 9)]
+    sets = [_case(12 + i, new, old, h_q, h_kv) for i, (new, old) in enumerate(shapes)]
+
+    def both(a):
+        q, kc, vc, cu, lens = a
+        return (qs.attn_prefill(q, cu, lens, kc, vc, h_q),
+                qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, plen_d, cu=cu))
+
+    want = [both(a) for a in sets]
+    for (new, old), a, w in zip(shapes, sets, want):
+        _check(w[0], new, old, a[0], a[1], a[2], h_q)
+        _check(w[1], new, old, a[0], a[1], a[2], h_q, pk, pv, plen)
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in sets], []
+
+    def run(i):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(100):
+                got[i].append(both(sets[i]))
+        except Exception as e:                              # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for i, outs in enumerate(got):
+        assert len(outs) == 100
+        for o in outs:
+            assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1]), i
+
+
+def test_default_stream_named_where_another_is_current(qs, fresh):
+    q, kc, vc, cu, lens = _case(21, [40, 300], [900, 0], 8, 2)
+    want = qs.attn_prefill(q, cu, lens, kc, vc, 8)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out = qs.attn_prefill(q, cu, lens, kc, vc, 8, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(fresh.of) == 1
+
+
+def test_workspace_that_is_outgrown_after_a_capture(qs, fresh):
+    """A small call eagerly, then captured, then a large one: the eager buffer is replaced and kept, the graph's
+    is its own, and the graph is right after others have taken what memory was free."""
+    h_q, h_kv, plen = 4, 2, 100
+    pk, pv = _prefix(22, h_kv, plen)
+    plen_d = _i32([plen])
+    small, big = _case(23, [1] * 4, [9] * 4, h_q, h_kv), _case(24, [1] * 400, [30] * 400, h_q, h_kv)
+    call = lambda c: qs.attn_prefix(c[0], c[4], 0, c[1], c[2], h_q, pk, pv, plen_d)   # noqa: E731
+    want = call(small)
+    (key, first), = fresh.of.items()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(small)
+    assert fresh.of[key] is first
+    _check(call(big), [1] * 400, [30] * 400, big[0], big[1], big[2], h_q, pk, pv, plen)
+    assert fresh.of[key].numel() > first.numel() and len(qs._PROMPT_WS_RETIRED) == 1
+    assert qs._PROMPT_WS_RETIRED[0] is first
+    fill = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        eager = call(small)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(eager, want)
+    assert all(bool((f == 255).all()) for f in fill)
+
+
+def test_status_of_the_default_workspace(qs, fresh):
+    """prompt_workspace is the buffer that calls without `work` report to; a captured call reports to its `work`."""
+    q, kc, vc, cu, lens = _case(25, [20, 30], [0, 4], 4, 2)
+    size = qs.attn_prefill_workspace_size()
+    qs.attn_prefill(q, cu, lens, kc, vc, 4)
+    ws = qs.prompt_workspace(size, "cuda")
+    assert ws is qs.prompt_workspace(256, q.device) and qs.workspace_status(ws) == 0
+    qs.attn_prefill(q, cu, lens - 1, kc, vc, 4)
+    assert qs.workspace_status(ws) == BAD_INPUT and qs.workspace_status(ws) == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    qs.attn_prefill(q, cu, lens - 1, kc, vc, 4, stream=side)
+    side.synchronize()
+    assert qs.workspace_status(ws) == 0
+    assert qs.workspace_status(qs.prompt_workspace(size, "cuda", stream=side), stream=side) == BAD_INPUT
+    work, wrong = torch.zeros(size, dtype=torch.uint8, device="cuda"), lens - 1
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qs.attn_prefill(q, cu, wrong, kc, vc, 4, work=work)
+    assert qs.workspace_status(work) == 0
+    graph.replay()
+    assert qs.workspace_status(work) == BAD_INPUT and qs.workspace_status(ws) == 0
