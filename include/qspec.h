@@ -347,8 +347,11 @@ qspec_status qspec_kv_commit(int32_t* lens, const int32_t* n_accepted, int32_t b
  * packed prompt is committed with n_accepted[b] = (its tokens) - 1.
  * Requires head_dim = 128, h_q a multiple of h_kv, 1 <= batch <= 65535,
  * n_tokens >= 1.  All reads of device-side lengths are checked: a sequence
- * whose cu entries or positions do not fit is skipped (its output rows zero)
- * and reported as QSPEC_ERR_BAD_INPUT through qspec_workspace_status.
+ * whose cu entries (below 0, decreasing, past n_tokens) or positions do not fit
+ * is skipped (the attention's rows zero, qspec_qkv_rope_append writes nothing) and
+ * reported as QSPEC_ERR_BAD_INPUT through qspec_workspace_status.  Where starts
+ * decrease, a token can lie in several sequences; qspec_qkv_rope_append then takes
+ * it for one of these, or for none, at that one's positions from lens[b] + offset on.
  * Asynchronous on `stream`; launched as programmatic dependents of the
  * preceding kernel, which they wait for before they read or write anything.
  */
@@ -375,7 +378,8 @@ qspec_status qspec_rope_table(const double* inv_freq, int32_t rot, int64_t posit
  *             turned in place (q_out = qkv, and ld_q = ld_qkv unless there is one token): the rows are
  *             then what qspec_attn_decode takes.  No other overlap.
  *  workspace  optional (NULL, or >= 256 zeroed bytes): the status word.  A token whose position is
- *             outside the cache or the table writes nothing and is reported there.
+ *             outside the cache or the table writes nothing and is reported there (the other tokens of its
+ *             sequence are written).
  * Requires rot a multiple of 8 in [0, 128], ld_qkv >= (h_q + 2 h_kv) * 128 and a multiple of 4,
  * ld_q >= h_q * 128 and a multiple of 8 (fp32: 4). */
 #define QSPEC_ROPE_INTERLEAVED 1u

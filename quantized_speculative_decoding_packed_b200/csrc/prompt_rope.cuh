@@ -70,12 +70,20 @@ __device__ __forceinline__ int find_sequence(const int32_t* __restrict__ cu, int
   return lo;
 }
 
-// grid (tokens, ceil((h_q + 2 h_kv) / kRopeHeadsPerCta))
+// grid (tokens, ceil((h_q + 2 h_kv) / kRopeHeadsPerCta)); with starts and a status word one column of CTAs
+// more, which looks at the starts (beside the loads of each token's own CTA the same test costs 2 us of 57).
 __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tok = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (tok >= a.n_tok) {
+    for (int e = threadIdx.x; e < a.batch && blockIdx.y == 0; e += kRopeWarps * 32) {
+      const int start = a.cu[e], end = a.cu[e + 1];
+      if (start < 0 || start > end || end > a.n_tok || (e == 0 && start != 0)) atomicOr(a.status, kDevBadInput);
+    }
+    return;
+  }
   const int heads = a.h_q + 2 * a.h_kv;
   const float* row = a.qkv + static_cast<int64_t>(tok) * a.ld + lane * 4;
   const int h0 = blockIdx.y * kRopeHeadsPerCta + warp;
@@ -92,27 +100,36 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qkv_rope_append_kernel(const 
   const int64_t pre = a.prefix_len ? *a.prefix_len : 0;
   int b, t;
   int64_t len;
-  if (a.cu && a.batch <= 31) {
-    // all starts and lengths at once, a lane each
-    const int start = lane <= a.batch ? a.cu[lane] : 0x7fffffff;
-    const int mine = lane < a.batch ? a.lens[lane] : 0;
-    if (tok >= __shfl_sync(0xffffffffu, start, a.batch)) return;       // rows behind the last sequence
-    const uint32_t le = __ballot_sync(0xffffffffu, lane < a.batch && start <= tok);
-    b = le ? 31 - __clz(le) : 0;                                       // the last that starts at or before it
-    t = tok - __shfl_sync(0xffffffffu, start, b);
-    len = __shfl_sync(0xffffffffu, mine, b);
-  } else if (a.cu) {
-    if (tok >= a.cu[a.batch]) return;
-    b = find_sequence(a.cu, a.batch, tok);
-    t = tok - a.cu[b];
-    len = a.lens[b];
+  if (a.cu) {
+    // (rows behind the last sequence, and tokens of one whose starts do not fit, are in none)
+    int start;
+    if (a.batch <= 31) {
+      // all starts and lengths at once, a lane each
+      const int mine = lane <= a.batch ? a.cu[lane] : -1;
+      const int cached = lane < a.batch ? a.lens[lane] : 0;
+      const int end = __shfl_down_sync(0xffffffffu, mine, 1);
+      const uint32_t in = __ballot_sync(0xffffffffu, static_cast<uint32_t>(mine) <= static_cast<uint32_t>(tok) &&
+                                                             tok < end && end <= a.n_tok);
+      if (in == 0) return;
+      b = 31 - __clz(in);
+      start = __shfl_sync(0xffffffffu, mine, b);
+      len = __shfl_sync(0xffffffffu, cached, b);
+    } else {
+      if (tok >= a.cu[a.batch]) return;
+      b = find_sequence(a.cu, a.batch, tok);
+      start = a.cu[b];
+      const int end = a.cu[b + 1];
+      len = a.lens[b];
+      if (start < 0 || tok < start || tok >= end || end > a.n_tok) return;
+    }
+    t = tok - start;
   } else {
     b = tok / a.t_new;
     t = tok - b * a.t_new;
     len = a.lens[b];
   }
   const int64_t pos = len + a.offset + t;
-  if (len < 0 || t < 0 || pos >= a.l_max || pre < 0 || (a.rot > 0 && pre + pos >= a.table_rows)) {
+  if (len < 0 || pos >= a.l_max || pre < 0 || (a.rot > 0 && pre + pos >= a.table_rows)) {
     if (a.status && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kDevBadInput);
     return;
   }

@@ -905,7 +905,8 @@ qspec_status qspec_qkv_rope_append(const float* qkv, int64_t ld_qkv, int64_t n_t
   a.l_max = l_max;
   a.interleaved = (flags & QSPEC_ROPE_INTERLEAVED) ? 1 : 0;
   a.q_f32 = q32 ? 1 : 0;
-  return launch_dependent(qkv_rope_append_kernel, dim3(static_cast<unsigned>(n_tokens), static_cast<unsigned>(slices)),
+  const int64_t columns = n_tokens + (cu && workspace ? 1 : 0);
+  return launch_dependent(qkv_rope_append_kernel, dim3(static_cast<unsigned>(columns), static_cast<unsigned>(slices)),
                           kRopeWarps * 32, 0, stream, a);
 }
 

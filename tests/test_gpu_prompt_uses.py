@@ -213,3 +213,61 @@ def test_status_of_the_default_workspace(qs, fresh):
     assert qs.workspace_status(work) == 0
     graph.replay()
     assert qs.workspace_status(work) == BAD_INPUT and qs.workspace_status(ws) == 0
+
+
+# ---------------------------------------------------------------- starts that do not fit
+STARTS = [
+    # starts of 3 sequences over 90 tokens; by sequence, tokens that are taken for it
+    ([0, 20, 10, 90], {0: (0, 10)}),
+    ([0, 20, 50, 91], {0: (0, 20), 1: (20, 50)}),
+    ([-5, 20, 50, 90], {1: (20, 50), 2: (50, 90)}),
+    ([0, 200, 50, 90], {}),
+    ([3, 20, 50, 90], {0: (3, 20), 1: (20, 50), 2: (50, 90)}),
+    ([0, 30, 30, 2 ** 31 - 1], {0: (0, 30)}),
+]
+
+
+@pytest.mark.parametrize("behind", [0, 60])
+@pytest.mark.parametrize("starts,fit", STARTS)
+def test_rope_append_reports_starts_that_do_not_fit(qs, starts, fit, behind):
+    """The call reports them, and a sequence that fits has its tokens as ever; nothing lies below its length, and
+    a sequence that does not fit writes nothing.  `behind`: that many more sequences, without tokens."""
+    g = _gen(31)
+    h_q, h_kv, n, l_max = 4, 2, 90, 300
+    starts = starts + [starts[-1]] * behind
+    batch = len(starts) - 1
+    lens = _i32([7, 3, 11] + [0] * behind)
+    qkv = _randn(g, n, (h_q + 2 * h_kv) * D, dtype=torch.float32)
+    table = _table(qs, 128, 400)
+    kc, vc = (torch.zeros(batch, h_kv, l_max, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.full((n, h_q * D), 9.0, dtype=torch.bfloat16, device="cuda")
+    work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qs.qkv_rope_append(qkv, lens, 0, kc, vc, h_q, table, cu=_i32(starts), q_out=q, work=work)
+    assert qs.workspace_status(work) == BAD_INPUT and qs.workspace_status(work) == 0
+    for b, (first, last) in fit.items():
+        one = [torch.zeros(1, h_kv, l_max, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        ref = qs.qkv_rope_append(qkv[first:last], lens[b:b + 1] + (first - starts[b]), 0, *one, h_q, table)
+        assert torch.equal(q[first:last], ref), b
+        at = slice(int(lens[b]) + first - starts[b], int(lens[b]) + last - starts[b])
+        assert torch.equal(kc[b, :, at], one[0][0, :, at]) and torch.equal(vc[b, :, at], one[1][0, :, at])
+    for b in range(3):
+        fits = 0 <= starts[b] <= starts[b + 1] <= n
+        assert not kc[b, :, :int(lens[b])].any() and not vc[b, :, :int(lens[b])].any()
+        if not fits:
+            assert not kc[b].any() and not vc[b].any()
+    for i in range(n):
+        if not any(0 <= starts[b] <= i < starts[b + 1] <= n for b in range(batch)):
+            assert bool((q[i] == 9).all()), i
+
+
+def test_rope_append_with_fitting_starts_reports_nothing(qs):
+    g = _gen(32)
+    for starts in ([0, 90], [0, 0, 40, 40, 90], [0] * 50 + [40, 40, 81], [0] * 300 + [7]):
+        batch = len(starts) - 1
+        qkv = _randn(g, 90, 3 * D, dtype=torch.float32)
+        kc, vc = (torch.zeros(batch, 1, 100, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        q = qs.qkv_rope_append(qkv, _i32([4] * batch), 0, kc, vc, 1, None, cu=_i32(starts), work=work,
+                               q_out=torch.full((90, D), 9.0, dtype=torch.bfloat16, device="cuda"))
+        assert qs.workspace_status(work) == 0
+        assert torch.equal(q[:starts[-1]], qkv[:starts[-1], :D].to(torch.bfloat16)) and bool((q[starts[-1]:] == 9).all())
