@@ -350,8 +350,9 @@ qspec_status qspec_kv_commit(int32_t* lens, const int32_t* n_accepted, int32_t b
  * whose cu entries (below 0, decreasing, past n_tokens) or positions do not fit
  * is skipped (the attention's rows zero, qspec_qkv_rope_append writes nothing) and
  * reported as QSPEC_ERR_BAD_INPUT through qspec_workspace_status.  Where starts
- * decrease, a token can lie in several sequences; qspec_qkv_rope_append then takes
- * it for one of these, or for none, at that one's positions from lens[b] + offset on.
+ * decrease, a token can lie in several sequences: the attention then zeroes all
+ * n_tokens rows; qspec_qkv_rope_append takes the token for one of the sequences, or
+ * for none, at that one's positions from lens[b] + offset on.
  * Asynchronous on `stream`; launched as programmatic dependents of the
  * preceding kernel, which they wait for before they read or write anything.
  */

@@ -73,7 +73,9 @@ struct PromptArgs {
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
 struct PaJoin {
-  int32_t valid, first, tok, tokens, g, pad[3];
+  int32_t valid, first, tok, tokens, g;
+  int32_t refused;             // (CTA 0's) the starts are out of order: every row is zero already
+  int32_t pad[2];
 };
 
 // Workspace: status word, what the GEMMs keep there, then per CTA two pieces of two row tiles
@@ -228,20 +230,22 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
 
 // ---------------------------------------------------------------- finding the items
 // Sequence b's packed tokens and the keys before them; n = 0 where its
-// offsets or its length are not those of the cache.
+// offsets or its length are not those of the cache.  Where starts fall, a row could belong to two
+// sequences (and be written by both): then the whole call is refused.
 struct PaSequence {
   int tok0, n, base;
-  bool bad;
+  bool bad, falls;             // falls: it ends before it starts
 };
 __device__ __forceinline__ PaSequence pa_sequence(const PromptArgs& a, int b) {
   PaSequence s;
   int n;
-  s.bad = false;
+  s.bad = s.falls = false;
   const int64_t len = a.lens[b];
   if (a.cu) {
     s.tok0 = a.cu[b];
     const int end = a.cu[b + 1];
-    s.bad = s.tok0 < 0 || end < s.tok0 || end > a.n_tok;
+    s.falls = end < s.tok0;
+    s.bad = s.tok0 < 0 || s.falls || end > a.n_tok;
     n = s.bad ? 0 : end - s.tok0;
   } else {
     s.tok0 = b * a.t_new;
@@ -300,6 +304,7 @@ struct PaShare {
   int64_t s0, s1, total;
   int64_t start;               // of the sequence in which the share begins
   int b, ctas;                 // b < 0: the prefix
+  bool refused;
 };
 
 // Barriers and small exchanges in shared memory.
@@ -358,8 +363,14 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
   const int64_t prefix_all = pa_run_cost(pa_prefix_run(a, prefix)) * a.h_kv;
   int64_t before = prefix_all;         // the cost before the chunk of sequences at hand
   int64_t cost = 0, at = 0;            // of one KV head of this thread's sequence; before the sequence
+  bool falls = false;
   auto scan = [&](int b) {
-    cost = b < a.batch ? pa_run_cost(pa_own_run(a, pa_sequence(a, b), prefix)) : 0;
+    cost = 0;
+    if (b < a.batch) {
+      const PaSequence s = pa_sequence(a, b);
+      falls = falls || s.falls;
+      cost = pa_run_cost(pa_own_run(a, s, prefix));
+    }
     const int64_t mine = cost * a.h_kv;
     int64_t incl = mine;
 #pragma unroll 1
@@ -382,7 +393,8 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
   };
 #pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) scan(b0 + tid);
-  const int64_t total = before;
+  const bool refused = __syncthreads_or(falls);
+  const int64_t total = refused ? 0 : before;
   const int ctas = working_ctas(total, gridDim.x), c = blockIdx.x;
   int64_t s0 = total, s1 = total;
   if (c < ctas && total > 0) share_of(total, ctas, c, &s0, &s1);
@@ -393,6 +405,7 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
     sm.share.ctas = ctas;
     sm.share.b = -1;
     sm.share.start = 0;
+    sm.share.refused = refused;
   }
   __syncthreads();
   before = prefix_all;
@@ -419,13 +432,17 @@ __device__ __forceinline__ void pa_find_share(const PromptArgs& a, PaShared& sm)
 // 1000 20.0 20.1 18.9, 4 x 1 behind a prefix of 500 15.7 13.9 13.9.
 constexpr int kPaPartTiles = 8;
 constexpr int kPaMinPart = 2;
-__device__ __forceinline__ int pa_find_one(const PromptArgs& a, PaItem* it) {
+__device__ __forceinline__ int pa_find_one(const PromptArgs& a, PaShared& sm, PaItem* it) {
   const int lane = threadIdx.x & 31;
   const int prefix = pa_prefix(a);
   PaSequence mine;
   mine.n = 0;
   mine.base = 0;
+  mine.falls = false;
   if (lane < a.batch) mine = pa_sequence(a, lane);
+  const bool refused = __any_sync(0xffffffffu, mine.falls);
+  if (lane == 0) sm.share.refused = refused;
+  if (refused) return 0;
   Run run = pa_prefix_run(a, prefix);
   const Run own = pa_own_run(a, mine, prefix);
   const int longest = max(run.n > 0 ? run.pre : 0,
@@ -495,7 +512,7 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
   if (a.parts > 0) {
     PaItem one;
-    const int there = pa_find_one(a, &one);
+    const int there = pa_find_one(a, sm, &one);
     if (there >= 0) {
       __syncthreads();           // the barriers are there (the other warps have waited for this one)
       if (there) pa_pass(sm, one, 0, status);
@@ -511,10 +528,12 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
   int b = -1, block = -1;
   int64_t total, s0, s1, start = 0, head_cost = prefix_head;
   int ctas;
+  bool falls = false;
   auto load = [&](int at) {
     if (at == block) return;
     block = at;
     mine.n = 0;
+    mine.falls = false;
     if (block * 32 + lane < a.batch) mine = pa_sequence(a, block * 32 + lane);
   };
   auto own_run = [&](int of) -> Run {
@@ -531,6 +550,7 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
     for (int half = 1; half >= 0; --half) {       // the first 32 last: they stay in `mine`
       if (half * 32 >= a.batch) continue;
       load(half);
+      falls = falls || mine.falls;
       const int64_t one = pa_run_cost(pa_own_run(a, mine, prefix));
       int64_t incl = one * a.h_kv;
 #pragma unroll 1
@@ -550,6 +570,9 @@ __device__ __forceinline__ void pa_find_items(const PromptArgs& a, PaShared& sm)
         total += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
+    falls = __any_sync(0xffffffffu, falls);
+    if (lane == 0) sm.share.refused = falls;
+    if (falls) total = 0;
     ctas = working_ctas(total, gridDim.x);
     s0 = s1 = total;
     if (blockIdx.x < ctas && total > 0) share_of(total, ctas, blockIdx.x, &s0, &s1);
@@ -1280,18 +1303,25 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
 }
 
 // Warp 11: what is refused is reported, its rows zero.
-__device__ __forceinline__ void pa_refuse(const PromptArgs& a) {
+__device__ __forceinline__ void pa_refuse(const PromptArgs& a, const PaShared& sm) {
   const int lane = threadIdx.x & 31;
   uint32_t* const status = reinterpret_cast<uint32_t*>(a.work);
-  const bool no_prefix = pa_prefix(a) < 0;
-  if (no_prefix && static_cast<int>(blockIdx.x) == 0 && lane == 0) atomicOr(status, kDevBadInput);
-  for (int b = static_cast<int>(blockIdx.x); b < a.batch; b += gridDim.x) {
-    const PaSequence s = pa_sequence(a, b);
-    if (!s.bad && !no_prefix) continue;
-    if (s.bad && lane == 0) atomicOr(status, kDevBadInput);
-    const int64_t t0 = s.tok0 < 0 ? 0 : s.tok0;
-    int64_t t1 = a.cu ? a.cu[b + 1] : t0 + a.t_new;
-    if (t1 > a.n_tok) t1 = a.n_tok;
+  const bool all = sm.share.refused, no_prefix = pa_prefix(a) < 0;
+  if (static_cast<int>(blockIdx.x) == 0 && lane == 0) {
+    reinterpret_cast<PaJoin*>(a.work + a.off_desc)->refused = all;
+    if (all || no_prefix) atomicOr(status, kDevBadInput);
+  }
+  // a sequence at a time; a row, where all are refused
+  for (int b = static_cast<int>(blockIdx.x); b < (all ? a.n_tok : a.batch); b += gridDim.x) {
+    int64_t t0 = b, t1 = t0 + 1;
+    if (!all) {
+      const PaSequence s = pa_sequence(a, b);
+      if (!s.bad && !no_prefix) continue;
+      if (s.bad && lane == 0) atomicOr(status, kDevBadInput);
+      t0 = s.tok0 < 0 ? 0 : s.tok0;
+      t1 = a.cu ? a.cu[b + 1] : t0 + a.t_new;
+      if (t1 > a.n_tok) t1 = a.n_tok;
+    }
     const int cols = a.h_q * (kHeadDim / 8);
     for (int64_t t = t0; t < t1; ++t)
       for (int e = lane; e < cols; e += 32)
@@ -1366,7 +1396,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (warp == 8) pa_load(a, sm, q_s, kv_s, &tm_q, &tm_k, &tm_v, &tm_pk, &tm_pv);
     if (warp == 9) pa_multiply(a, sm, tmem, q_s, kv_s);
     if (warp == 10) pa_find_items(a, sm);
-    if (warp == 11) pa_refuse(a);
+    if (warp == 11) pa_refuse(a, sm);
   }
   tc_fence_before();
   __syncthreads();
@@ -1460,6 +1490,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   const int prefix = pa_prefix(a);
   int b;
   if (a.cu) {
+    if (reinterpret_cast<const PaJoin*>(a.work + a.off_desc)->refused) return;
     if (tok >= a.cu[a.batch] || tok < a.cu[0]) return;
     b = find_sequence(a.cu, a.batch, tok);
   } else {
@@ -1473,7 +1504,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   const int in0 = tok % (2 * a.tpt), in1 = t < 2 * a.tpt ? t : t % (2 * a.tpt);     // the token's place in its item
   const int2 c0 = prefix > 0 ? owners[static_cast<int64_t>(tok - in0) * a.h_kv + g] : make_int2(0, -1);
   const int2 c1 = owners[static_cast<int64_t>(a.n_tok) * a.h_kv + static_cast<int64_t>(tok - in1) * a.h_kv + g];
-  // (what a call that gave up, or whose starts are not in order, has left out is not followed)
+  // (what a call that gave up has left out is not followed)
   auto sound = [&](int2 c) { return c.x >= 0 && c.x <= c.y && c.y < a.ctas; };
   if ((prefix > 0 && !sound(c0)) || !sound(c1)) return;
   const int n0 = c0.y - c0.x + 1, n = n0 + c1.y - c1.x + 1;

@@ -271,3 +271,42 @@ def test_rope_append_with_fitting_starts_reports_nothing(qs):
                                q_out=torch.full((90, D), 9.0, dtype=torch.bfloat16, device="cuda"))
         assert qs.workspace_status(work) == 0
         assert torch.equal(q[:starts[-1]], qkv[:starts[-1], :D].to(torch.bfloat16)) and bool((q[starts[-1]:] == 9).all())
+
+
+@pytest.mark.parametrize("behind", [0, 40, 70])
+@pytest.mark.parametrize("starts", [[0, 20, 10, 90], [0, 90, 0, 90], [0, 50, 49, 49], [-5, 60, 20, 300], [0, 20, 2 ** 31 - 1, 3]])
+def test_attention_refuses_starts_out_of_order(qs, starts, behind):
+    """Where starts fall a row could belong to two sequences: every row is zero, and the call is reported; the next
+    call on the same workspace is as ever.  `behind`: that many more sequences without tokens."""
+    new, old, h_q, h_kv, plen = [20, 30, 40], [500, 4, 8], 8, 2, 300
+    q, kc, vc, cu, lens = _case(33, new + [0] * behind, old + [0] * behind, h_q, h_kv)
+    pk, pv = _prefix(34, h_kv, plen)
+    bad = _i32(starts + [starts[-1]] * behind)
+    batch = 3 + behind
+
+    def calls(cu, work, out):
+        yield lambda: qs.attn_prefill(q, cu, lens, kc, vc, h_q, work=work, out=out)
+        yield lambda: qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=work, out=out)
+
+    size = max(qs.attn_prefill_workspace_size(), qs.attn_prefix_workspace_size(90, batch, h_q, h_kv))
+    work = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for wrong, right, p in zip(calls(bad, work, out := torch.full_like(q, 3.0)), calls(cu, work, None), (0, plen)):
+        out.fill_(3)
+        wrong()
+        assert qs.workspace_status(work) == BAD_INPUT and qs.workspace_status(work) == 0
+        assert bool((out == 0).all())
+        _check(right(), new + [0] * behind, old + [0] * behind, q, kc, vc, h_q, pk, pv, p)
+        assert qs.workspace_status(work) == 0
+
+
+def test_attention_refuses_starts_out_of_order_behind_a_prefix_taken_ahead(qs):
+    new, old, h_q, h_kv, plen = [100, 130, 200], [500, 4, 8], 8, 2, 300
+    q, kc, vc, cu, lens = _case(35, new, old, h_q, h_kv)
+    pk, pv = _prefix(36, h_kv, plen)
+    work = torch.zeros(qs.attn_prefix_workspace_size(430, 3, h_q, h_kv), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 3.0)
+    qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=_i32([0, 300, 200, 430]), work=work, out=out)
+    assert qs.workspace_status(work) == BAD_INPUT and bool((out == 0).all())
+    qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=work, out=out)
+    assert qs.workspace_status(work) == 0
+    _check(out, new, old, q, kc, vc, h_q, pk, pv, plen)
