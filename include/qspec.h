@@ -401,7 +401,11 @@ qspec_status qspec_qkv_rope_append(const float* qkv, int64_t ld_qkv, int64_t n_t
  *  workspace  >= qspec_attn_prefill_workspace_size() bytes, 16-byte aligned; its first 4 bytes zero
  *             before the first use.  Calls sharing one workspace must not overlap.
  * Scores, softmax statistics and sums in fp32; the softmax weights are rounded to bf16 before they meet
- * the bf16 values.  What is stored past the last position that a sequence sees does not matter, not even NaN.
+ * the bf16 values, and a quarter of them come from a cubic with a relative error of 7.5e-5 (1/26 of that
+ * rounding's).  What is stored past the last position that a sequence sees does not matter, not even NaN.
+ * A score of NaN or +inf makes its row NaN, one of -inf weighs nothing.  A value that is not finite
+ * reaches every row of its tiles, rows of the same sequence that do not see it among them (0 times it
+ * is NaN): values must be finite up to the last position that the sequence sees.
  * Requires h_q / h_kv <= 128, ld_q and ld_out >= h_q * 128 and multiples of 8. */
 qspec_status qspec_attn_prefill(const uint16_t* q, int64_t ld_q, int64_t n_tokens, int32_t batch, const int32_t* cu,
                                 int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens,

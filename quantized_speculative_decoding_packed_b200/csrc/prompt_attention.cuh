@@ -203,6 +203,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
   return d;
 }
+// The largest, or NaN where one of them is NaN.
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
 // One of so many pairs of weights comes from exp2_poly: the special function unit, at 4 a cycle for
 // each quarter of an SM, takes 1024 cycles for a warp's tile alone.  Cycles for the weights of a tile,
 // by the share of pairs: none 1400, an eighth 1200, a quarter 1060, three eighths 1190, half 1550.
@@ -1076,8 +1082,8 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         auto largest = [&](const uint32_t* x) {
           float t[2] = {top, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) t[(e >> 1) & 1] = max3(t[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          top = fmaxf(t[0], t[1]);
+          for (int e = 0; e < 32; e += 2) t[(e >> 1) & 1] = max3_nan(t[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          top = max3_nan(t[0], t[1], t[1]);
         };
         tmem_ld32(s_t, u[0]);
 #pragma unroll 1
@@ -1091,9 +1097,11 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         }
         tmem_ld_wait();
         tmem_ld32(s_t, u[0]);
-        const bool raise = (top - m) * kScoreLog2 > kRaise;           // false where both are -inf
+        // (a score of NaN or +inf makes the row's maximum, and with it all of the row, NaN)
+        const bool raise = live && top != -INFINITY && !((top - m) * kScoreLog2 <= kRaise);
         float f = 1.f;
         if (__any_sync(0xffffffffu, raise)) {
+          if (top == INFINITY) top = NAN;
           f = raise ? ex2((m - top) * kScoreLog2) : 1.f;
           l *= f;
           if (raise) m = top;
@@ -1216,7 +1224,7 @@ __device__ __forceinline__ void pa_output(const PromptArgs& a, PaShared& sm, uin
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.ml_free[1]));
       }
-      const float m = fmaxf(ml0.x, ml1.x);
+      const float m = max3_nan(ml0.x, ml1.x, ml1.x);
       float f0 = ml0.x == -INFINITY ? 0.f : ex2((ml0.x - m) * kScoreLog2);
       float f1 = ml1.x == -INFINITY ? 0.f : ex2((ml1.x - m) * kScoreLog2);
       const float l = ml0.y * f0 + ml1.y * f1;
@@ -1454,7 +1462,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
     for (int e = 0; e < 2; ++e) {
       const float w = pa_piece_weight(s[e].x, top);
       l = fmaf(s[e].y, w, l);
-      if (w > 0.f) {
+      if (w != 0.f) {                  // (NaN too)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           acc[k].x = fmaf(v[e][k].x, w, acc[k].x);
@@ -1557,7 +1565,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (wq[e] > 0.f) {
+        if (wq[e] != 0.f) {                            // (NaN too)
           acc.x = fmaf(v[e].x, wq[e], acc.x);
           acc.y = fmaf(v[e].y, wq[e], acc.y);
           acc.z = fmaf(v[e].z, wq[e], acc.z);

@@ -310,3 +310,78 @@ def test_attention_refuses_starts_out_of_order_behind_a_prefix_taken_ahead(qs):
     qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=work, out=out)
     assert qs.workspace_status(work) == 0
     _check(out, new, old, q, kc, vc, h_q, pk, pv, plen)
+
+
+# ---------------------------------------------------------------- values that are not finite
+def _all_kinds(qs, q, kc, vc, lens, new, h_q, pk, pv, plen):
+    """(name, output) of each way that a batch can go: whole items, split ones, a prefix ahead and once."""
+    cu = _i32([sum(new[:i]) for i in range(len(new) + 1)])
+    yield "prefill", 0, qs.attn_prefill(q, cu, lens, kc, vc, h_q)
+    yield "prefix", plen, qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu)
+
+
+NOT_FINITE = [
+    # new, cached, h_q, h_kv, prefix: few items, shares, pieces, one row tile, two, prefix once and ahead
+    ([5, 3], [30, 200], 4, 2, 40),
+    ([200], [0], 4, 4, 300),
+    ([3], [9000], 2, 1, 12000),
+    ([1, 1, 1, 1], [5, 300, 2000, 128], 8, 8, 500),
+    ([400, 300], [100, 0], 8, 2, 700),
+    ([1] * 70, [33] * 70, 4, 2, 200),
+]
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new,old,h_q,h_kv,plen", NOT_FINITE)
+def test_a_score_that_is_not_finite_makes_its_row_nan(qs, new, old, h_q, h_kv, plen, what):
+    """softmax of scores with a NaN or +inf is NaN: for the rows that see the key, and for no others.  Keys at
+    every place modulo 8 of a tile are tried (weights come from two kinds of exponentials)."""
+    q, kc, vc, cu, lens = _case(51, new, old, h_q, h_kv)
+    q = q.abs() + 0.125                                     # so that a key of +inf has a score of +inf
+    pk, pv = _prefix(52, h_kv, plen)
+    want = {name: out for name, _, out in _all_kinds(qs, q, kc, vc, lens, new, h_q, pk, pv, plen)}
+    group, starts = h_q // h_kv, [sum(new[:i]) for i in range(len(new))]
+    last = len(new) - 1
+    for back in range(min(9, new[last] + old[last])):
+        at = old[last] + new[last] - 1 - back               # a key of the last sequence's, of its last KV head
+        kc[last, h_kv - 1, at, 7], kept = what, kc[last, h_kv - 1, at, 7].clone()
+        for name, _, out in _all_kinds(qs, q, kc, vc, lens, new, h_q, pk, pv, plen):
+            nan = torch.zeros_like(out, dtype=torch.bool)
+            first = max(0, at - old[last])                  # the first token that sees it
+            nan[starts[last] + first:, (h_q - group) * D:] = True
+            assert torch.equal(out.isnan(), nan), (name, back)
+            assert torch.equal(out[~nan], want[name][~nan]), (name, back)
+        kc[last, h_kv - 1, at, 7] = kept
+    for place in (0, plen // 2, plen - 1):                  # a key of the prefix: all rows of its heads
+        pk[0, place, 3], kept = what, pk[0, place, 3].clone()
+        out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu)
+        assert bool(out[:, :group * D].isnan().all()), place
+        assert torch.equal(out[:, group * D:], want["prefix"][:, group * D:])
+        pk[0, place, 3] = kept
+
+
+@pytest.mark.parametrize("new,old,h_q,h_kv,plen", NOT_FINITE)
+def test_a_query_that_is_not_finite_makes_its_row_nan(qs, new, old, h_q, h_kv, plen):
+    q, kc, vc, cu, lens = _case(53, new, old, h_q, h_kv)
+    pk, pv = _prefix(54, h_kv, plen)
+    want = {name: out for name, _, out in _all_kinds(qs, q, kc, vc, lens, new, h_q, pk, pv, plen)}
+    for tok, head in ((0, 0), (sum(new) - 1, h_q - 1), (sum(new) // 2, h_q // 2)):
+        bad = q.clone()
+        bad[tok, head * D + 5] = float("nan")
+        for name, _, out in _all_kinds(qs, bad, kc, vc, lens, new, h_q, pk, pv, plen):
+            nan = torch.zeros_like(out, dtype=torch.bool)
+            nan[tok, head * D:(head + 1) * D] = True
+            assert torch.equal(out.isnan(), nan), (name, tok, head)
+            assert torch.equal(out[~nan], want[name][~nan]), (name, tok, head)
+
+
+def test_scores_of_minus_infinity_weigh_nothing(qs):
+    """Keys whose score is -inf, alone and beside others: weight 0; a row with no other key is zero."""
+    new, old, h_q, h_kv = [3], [300], 2, 1
+    q, kc, vc, cu, lens = _case(55, new, old, h_q, h_kv)
+    q = q.abs() + 0.125
+    kc[0, 0, :100, 9] = -float("inf")
+    out = qs.attn_prefill(q, cu, lens, kc, vc, h_q)
+    _check(out, new, [200], q, kc[:, :, 100:], vc[:, :, 100:], h_q)
+    kc[0, 0, :303, 9] = -float("inf")
+    assert not qs.attn_prefill(q, cu, lens, kc, vc, h_q).any()
