@@ -198,6 +198,16 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return d;
 }
 
+// (subnormal terms and sums count as 0)
+__device__ __forceinline__ float2 add2_ftz(float2 x, float2 y) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.ftz.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return d;
+}
+
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
@@ -219,6 +229,9 @@ constexpr int kPolyEach = 4;
 // polynomial, k added to its exponent.  The polynomial is the one of degree 3
 // with the least relative error on |r| <= 1/2 (7.5e-5, from a weighted
 // least-squares fit): 1/26 of half a step of the bf16 that its result becomes.
+// x <= -126 (a key that is not seen has -inf) is taken as -126, whose power by the cubic, 0.99996 2^-126, is
+// subnormal: the addition at the end makes it 0, as ex2 has it.  (Kept, such a weight brings 1.2 into the
+// output for a value of 10^38 that the row does not see.)
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);
@@ -231,7 +244,7 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
   y = fma2(y, r, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
   y.x = __int_as_float((__float_as_int(t.x) << 23) + __float_as_int(y.x));
   y.y = __int_as_float((__float_as_int(t.y) << 23) + __float_as_int(y.y));
-  return y;
+  return add2_ftz(y, make_float2(0.f, 0.f));
 }
 
 // ---------------------------------------------------------------- finding the items
@@ -1060,8 +1073,7 @@ __device__ __forceinline__ void pa_softmax(const PromptArgs& a, PaShared& sm, ui
         const int lim = (in_pre ? pre_sees : own_sees) - at;
         // Columns from `seen` on no row of the warp sees: neither read nor weighed, their P is 0.  Before
         // that, where some row does not see some column, -inf goes into S (a small loop for what is rare:
-        // the warps of all roles share the instruction caches).  exp2_poly makes 2^-126 of -inf: nothing
-        // beside the largest weight of any row, and a row without any is known by its m.
+        // the warps of all roles share the instruction caches).
         int seen = 128;
         if (partly) {
           seen = __reduce_max_sync(0xffffffffu, max(min(lim, 128), 0));

@@ -385,3 +385,33 @@ def test_scores_of_minus_infinity_weigh_nothing(qs):
     _check(out, new, [200], q, kc[:, :, 100:], vc[:, :, 100:], h_q)
     kc[0, 0, :303, 9] = -float("inf")
     assert not qs.attn_prefill(q, cu, lens, kc, vc, h_q).any()
+
+
+def test_values_behind_a_row_weigh_nothing(qs):
+    """Values of 2^127 at positions that a row does not see, and at seen ones whose weight is 2^-220 or less of the
+    largest (0 in fp32): the rows' outputs are those of the keys that weigh.  Every place modulo 8."""
+    for new, old, h_q, h_kv, plen in (([24], [0], 2, 1, 50), ([24], [300], 2, 1, 130), ([150], [40], 4, 4, 10)):
+        q, kc, vc, cu, lens = _case(56, new, old, h_q, h_kv)
+        pk, pv = _prefix(57, h_kv, plen)
+        m, o = new[0], old[0]
+        late = m - 17                                       # the last 16 tokens and theirs alone are large
+        kc[0, :, :o + m] *= 0.125
+        clean = vc.clone()
+        clean[0, :, o + late + 1:o + m] = 0
+        for i in range(late + 1, m):
+            vc[0, :, o + i] = 2.0 ** 127
+        for name, p, out in _all_kinds(qs, q, kc, vc, lens, new, h_q, pk, pv, plen):
+            ref = dict((n, x) for n, _, x in _all_kinds(qs, q, kc, clean, lens, new, h_q, pk, pv, plen))[name]
+            assert torch.equal(out[:late + 1], ref[:late + 1]), (name, new)
+            _check(ref[:late + 1], [late + 1], old, q[:late + 1], kc, clean, h_q, pk, pv, p)
+    # keys that are seen, with scores 300 below the others (2^-432)
+    q, kc, vc, cu, lens = _case(58, [20], [200], 2, 2)
+    q[:, 0::D] = 64.0
+    kc[0, :, :220, 0] = 0
+    kc[0, :, :40, 0] = -53.0                                # -53 64 / sqrt(128) = -299.8
+    clean = vc.clone()
+    clean[0, :, :40] = 0
+    vc[0, :, :40] = 2.0 ** 127
+    out, ref = qs.attn_prefill(q, cu, lens, kc, vc, 2), qs.attn_prefill(q, cu, lens, kc, clean, 2)
+    assert torch.equal(out, ref)
+    _check(ref, [20], [200], q, kc, clean, 2)
