@@ -497,9 +497,9 @@ size_t qspec_workspace_size(int32_t op, int64_t m, int64_t n, int64_t k, int32_t
 /* Synchronizes `stream`, reads the device status word at the start of
  * `workspace`, clears it, and returns QSPEC_OK, QSPEC_ERR_TIMEOUT or
  * QSPEC_ERR_BAD_INPUT (or QSPEC_ERR_CUDA if the read itself failed).  After
- * a timeout (which only a GEMM reports) it also clears the split-tile
- * tickets the stopped call may have left taken, so the workspace is ready
- * for the next call. */
+ * a GEMM's timeout it also clears the split-tile tickets that the stopped call
+ * may have left taken, so that the workspace is ready for the next call (an
+ * attention that timed out leaves nothing to clear). */
 qspec_status qspec_workspace_status(void* workspace, void* stream);
 
 /* Version of this ABI (3: adds QSPEC_GEMM_TEST_STALL, qspec_gemm_w4a8, qspec_cast_bf16,

@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kAttnThreads, 4) attn_decode_kernel(const Attn
     *reinterpret_cast<float4*>(q_s + e) = v;
   }
   __syncthreads();
-  const bool ok = __syncthreads_and(n_keys == 0 || mbar_wait(bar, 0, &abort_flag, status));
+  const bool ok = __syncthreads_and(n_keys == 0 || mbar_wait(bar, 0, &abort_flag, nullptr));
   if (!ok && tid == 0) {
+    atomicOr(status, kDevStopped);
     // the copies did not land in time (reported): let them finish before
     // the shared memory is released, and leave an empty partial
     mbar_wait_drain(bar, 0);

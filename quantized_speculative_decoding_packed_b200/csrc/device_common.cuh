@@ -59,6 +59,7 @@ namespace qspec {
 // Device status bits written to the first word of a workspace.
 constexpr uint32_t kDevTimeout = 1u;
 constexpr uint32_t kDevBadInput = 2u;
+constexpr uint32_t kDevStopped = 4u;     // a wait that ran out in a kernel that leaves nothing to clear
 
 // A wait that has not completed after this long is treated as a fault.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;   // 1 s

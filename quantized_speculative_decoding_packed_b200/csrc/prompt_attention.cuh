@@ -167,7 +167,7 @@ __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, volatile 
     const uint64_t now = global_timer_ns();
     if (start == 0) start = now;
     if (*abort_flag || now - start > kWaitLimitNs) {
-      if (!*abort_flag) atomicOr(status, kDevTimeout);
+      if (!*abort_flag) atomicOr(status, kDevStopped);
       *abort_flag = 1;
       break;
     }
@@ -1359,7 +1359,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t q_s = smem_u32(pa_dyn), kv_s = q_s + 2 * kPaTileBytes;
   if (q_s & 1023u) {                     // the swizzled tiles count on it
-    if (tid == 0) atomicOr(reinterpret_cast<uint32_t*>(a.work), kDevTimeout);
+    if (tid == 0) atomicOr(reinterpret_cast<uint32_t*>(a.work), kDevStopped);
     return;
   }
 

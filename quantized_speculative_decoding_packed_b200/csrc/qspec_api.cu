@@ -1038,17 +1038,18 @@ qspec_status qspec_workspace_status(void* workspace, void* stream) {
     return QSPEC_ERR_CUDA;
   }
   if (word == 0) return QSPEC_OK;
-  // A GEMM that gave up (the only kernels that time out) may have left
-  // split-tile tickets taken: clear them with the status word, so that the
-  // workspace is ready for the next call.  An accept workspace (256 bytes)
-  // only ever receives BAD_INPUT.
+  // A GEMM that gave up may have left split-tile tickets taken: clear them
+  // with the status word, so that the workspace is ready for the next call.
+  // The other kernels' workspaces can end before the tickets would (256
+  // bytes for accept, 1280 for a small attn_decode), and an attention that
+  // gave up leaves nothing to clear.
   const size_t clear = (word & kDevTimeout) ? kStatusAndTicketBytes : 4;
   if (cudaMemsetAsync(workspace, 0, clear, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();
     return QSPEC_ERR_CUDA;
   }
-  return (word & kDevTimeout) ? QSPEC_ERR_TIMEOUT : QSPEC_ERR_BAD_INPUT;
+  return (word & (kDevTimeout | kDevStopped)) ? QSPEC_ERR_TIMEOUT : QSPEC_ERR_BAD_INPUT;
 }
 
 // ---------------------------------------------------------------- no-allocation variant

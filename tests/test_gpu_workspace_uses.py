@@ -130,3 +130,16 @@ def test_captured_first_then_eager_then_grown(qs, fresh):
     assert torch.equal(_call(qs, a), want_a) and torch.equal(_call(qs, big), want_big)
     torch.cuda.synchronize()
     assert all(bool((f == 255).all()) for f in fill)
+
+
+def test_status_of_a_stopped_attention_clears_its_word_alone(qs):
+    """An attn_decode workspace can be smaller than the GEMMs' tickets, which a GEMM's timeout clears: what an
+    attention reports (bit 2 of the word) is read and cleared, and nothing behind the word is written."""
+    need = qs.attn_workspace_size(1, 1, 1, 1, 50)
+    assert need < 4352
+    for word, status in ((4, 5), (6, 5), (2, 6)):
+        buffer = torch.full((8192,), 7, dtype=torch.uint8, device="cuda")
+        buffer[:4] = torch.tensor([word, 0, 0, 0], dtype=torch.uint8)
+        assert qs.workspace_status(buffer[:need]) == status
+        assert not buffer[:4].any() and bool((buffer[4:] == 7).all())
+        assert qs.workspace_status(buffer[:need]) == 0
