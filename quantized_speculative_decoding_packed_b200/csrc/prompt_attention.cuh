@@ -69,6 +69,7 @@ struct PromptArgs {
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
   int ctas;                    // of the attention's grid
   int parts;                   // > 0: few items (and batch <= 32), each can have so many CTAs of its own
+  uint32_t test_stall_ns;      // test hook (0 = off): the loads first wait so long for what nobody signals
 };
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
@@ -699,7 +700,11 @@ __device__ __forceinline__ void pa_load(const PromptArgs& a, PaShared& sm, uint3
   const uint32_t leader = elect_one_lane();
   uint32_t ring = 0, qn = 0;
   bool ok = true;
-  for (uint32_t count = 0;; ++count) {
+  if (a.test_stall_ns != 0u) {
+    ok = __all_sync(0xffffffffu, mbar_wait_slow(smem_u32(&sm.drained), 0, abort_flag, nullptr, a.test_stall_ns));
+    if (!ok) atomicOr(status, kDevStopped);
+  }
+  for (uint32_t count = 0; ok; ++count) {
     ok = pa_item_wait(sm, count, status);
     if (!ok) break;
     const PaItem it = sm.items[count % kPaItems];
@@ -1359,7 +1364,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t q_s = smem_u32(pa_dyn), kv_s = q_s + 2 * kPaTileBytes;
   if (q_s & 1023u) {                     // the swizzled tiles count on it
-    if (tid == 0) atomicOr(reinterpret_cast<uint32_t*>(a.work), kDevStopped);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) {
+      atomicOr(reinterpret_cast<uint32_t*>(a.work), kDevStopped);
+      (reinterpret_cast<PaJoin*>(a.work + a.off_desc) + static_cast<int>(blockIdx.x))->valid = 0;
+    }
     return;
   }
 

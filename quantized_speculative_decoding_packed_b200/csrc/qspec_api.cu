@@ -440,7 +440,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
                                   const uint16_t* k_cache, const uint16_t* v_cache, int32_t l_max, bool with_prefix,
                                   const uint16_t* prefix_k, const uint16_t* prefix_v, int32_t prefix_max,
                                   const int32_t* prefix_len, uint16_t* out, int64_t ld_out, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+                                  size_t workspace_bytes, void* stream, bool test_stall = false) {
   if (!q || !lens || !k_cache || !v_cache || !out || !workspace) return QSPEC_ERR_INVALID_ARG;
   if (with_prefix && (!prefix_k || !prefix_v || !prefix_len || prefix_max < 1 || prefix_max > 0x7FFFFFFF - 256))
     return QSPEC_ERR_INVALID_ARG;
@@ -509,6 +509,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   const int64_t most_tiles = (static_cast<int64_t>(l_max) + 127) / 128 + (with_prefix ? (static_cast<int64_t>(prefix_max) + 127) / 128 : 0);
   const bool unsplit = a.parts > 0 && (most_tiles <= kPaMinPart || (a.parts == 1 && most_tiles <= kPaPartTiles));
   a.ctas = grid;
+  a.test_stall_ns = test_stall ? 10u * 1000u * 1000u : 0u;   // 10 ms
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
   const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};
@@ -976,6 +977,8 @@ qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* st
                                  positions, rot, prefix_len, lens, offset, k_cache, v_cache, l_max, q_out, ld_q,
                                  static_cast<uint32_t>(flags), workspace, static_cast<size_t>(bytes), stream);
   }
+  const bool stall = call >= 0 && (call & QSPEC_CALL_TEST_STALL) != 0;
+  if (stall) call &= ~QSPEC_CALL_TEST_STALL;
   const bool prefix = call == QSPEC_CALL_ATTN_PREFIX && n_args == 21;
   if (!prefix && !(call == QSPEC_CALL_ATTN_PREFILL && n_args == 16)) return QSPEC_ERR_INVALID_ARG;
   const uint16_t* q = p.ptr<const uint16_t>();
@@ -997,11 +1000,10 @@ qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* st
   void* workspace = p.ptr<void>();
   const int64_t bytes = p.next();
   if (!p.ok || bytes < 0) return QSPEC_ERR_INVALID_ARG;
-  return prefix ? qspec_attn_prefix(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, offset, k_cache, v_cache,
-                                    l_max, prefix_k, prefix_v, prefix_max, prefix_len, out, ld_out, workspace,
-                                    static_cast<size_t>(bytes), stream)
-                : qspec_attn_prefill(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, k_cache, v_cache, l_max,
-                                     out, ld_out, workspace, static_cast<size_t>(bytes), stream);
+  if (!prefix && !cu) return QSPEC_ERR_INVALID_ARG;
+  return run_prompt_attention(q, ld_q, n_tokens, batch, cu, h_q, h_kv, head_dim, lens, offset, k_cache, v_cache, l_max,
+                              prefix, prefix_k, prefix_v, prefix_max, prefix_len, out, ld_out, workspace,
+                              static_cast<size_t>(bytes), stream, stall);
 }
 
 size_t qspec_workspace_size(int32_t op, int64_t m, int64_t n, int64_t k, int32_t group,

@@ -42,3 +42,11 @@ def test_row_strides_of_the_binding(lib):
     assert rows(wide[:1].expand(3, 1037)[:1], 1, 512) == (wide.data_ptr(), 512)
     with pytest.raises(ValueError):
         rows(wide[:, ::2], 3, 512)
+
+
+def test_test_hook_of_the_attention_calls(lib):
+    """The hook's bit belongs to the two attention calls; what these refuse, they refuse with it."""
+    bad = [0x10000, 512, 6, 2, 0x10000, 4, 2, 64, 0x10000, 0x10000, 0x10000, 8, 0x10000000000, 512, 0x10000, 1 << 40]
+    call = lambda op, n: lib.LIB.qspec_call(op, lib._PREFILL_ARGS.pack(*bad), n, None)      # noqa: E731
+    for op, n in ((1, 16), (0x101, 16), (0x101, 15), (0x100, 16), (0x103, 16), (0x201, 16), (-0xff, 16)):
+        assert call(op, n) == INVALID_ARG
