@@ -446,7 +446,11 @@ enum {
 };
 qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* stream);
 
-/* Bytes of workspace on the current device (0: invalid arguments or device). */
+/* Bytes of workspace on the current device (0: invalid arguments or device).  The prefix's does not only
+ * grow with n_tokens: it falls where the prefix goes ahead of each sequence's own keys, from
+ * floor(n_tokens / batch) * (h_q / h_kv) >= 96 on, since rows of it and of own keys no longer lie apart.
+ * A workspace for all calls of up to N tokens of one batch is the larger of the size for N and, where N is
+ * that far, for batch * ceil(96 / (h_q / h_kv)) - 1 tokens. */
 size_t qspec_attn_prefill_workspace_size(void);
 size_t qspec_attn_prefix_workspace_size(int64_t n_tokens, int32_t batch, int32_t h_q, int32_t h_kv);
 

@@ -586,7 +586,11 @@ def attn_prefill_workspace_size() -> int:
 
 
 def attn_prefix_workspace_size(n_tokens: int, batch: int, h_q: int, h_kv: int) -> int:
-    """Bytes that attn_prefix needs on the current device (0: invalid shape, or it does not run)."""
+    """Bytes that attn_prefix needs on the current device (0: invalid shape, or it does not run).
+
+    Fewer tokens can need more: the size falls where the prefix goes ahead of each sequence's own keys
+    (n_tokens // batch * (h_q // h_kv) >= 96); the largest below is for batch * ceil(96 / (h_q // h_kv)) - 1.
+    """
     return int(LIB.qspec_attn_prefix_workspace_size(n_tokens, batch, h_q, h_kv))
 
 

@@ -415,3 +415,33 @@ def test_values_behind_a_row_weigh_nothing(qs):
     out, ref = qs.attn_prefill(q, cu, lens, kc, vc, 2), qs.attn_prefill(q, cu, lens, kc, clean, 2)
     assert torch.equal(out, ref)
     _check(ref, [20], [200], q, kc, clean, 2)
+
+
+@pytest.mark.parametrize("batch,h_q,h_kv", [(64, 32, 8), (3, 14, 2), (5, 8, 8), (2, 100, 1), (4, 200, 2)])
+def test_prefix_workspace_size_over_token_counts(qs, batch, h_q, h_kv):
+    """The documented rule: it falls at one number of tokens, and the size there or for the largest covers all."""
+    each = -(-96 // (h_q // h_kv))                          # tokens a sequence from which the prefix goes ahead
+    sizes = [qs.attn_prefix_workspace_size(n, batch, h_q, h_kv) for n in range(1, 4 * batch * each)]
+    peak = batch * each - 1
+    falls = [n for n in range(1, len(sizes)) if sizes[n] < sizes[n - 1]]
+    assert falls == ([peak] if peak > 0 else []) and max(sizes) == (sizes[peak - 1] if peak > 0 else sizes[-1])
+    assert min(sizes) >= qs.attn_prefill_workspace_size()
+
+
+def test_one_workspace_for_all_token_counts(qs):
+    """Calls on both sides of the fall on one buffer of the documented size; a smaller one is refused."""
+    batch, h_q, h_kv, plen = 4, 8, 2, 200
+    pk, pv = _prefix(61, h_kv, plen)
+    size = qs.attn_prefix_workspace_size(batch * 24 - 1, batch, h_q, h_kv)
+    assert size > qs.attn_prefix_workspace_size(batch * 24, batch, h_q, h_kv)
+    work = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for new in ([24] * 4, [24, 24, 24, 23], [1] * 4, [40] * 4, [24, 24, 24, 23]):
+        old = [30] * 4
+        q, kc, vc, cu, lens = _case(62, new, old, h_q, h_kv)
+        out = qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=work)
+        _check(out, new, old, q, kc, vc, h_q, pk, pv, plen)
+    assert qs.workspace_status(work) == 0
+    small = work[:qs.attn_prefix_workspace_size(batch * 24, batch, h_q, h_kv)]
+    with pytest.raises(qs.QSpecError) as e:
+        qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=small)
+    assert e.value.status == 4
