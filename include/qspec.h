@@ -344,7 +344,10 @@ qspec_status qspec_kv_commit(int32_t* lens, const int32_t* n_accepted, int32_t b
  * cu[batch] on are padding: not read for any result, never written.  With cu
  * NULL (where allowed) every sequence has n_tokens / batch of them.  Token i
  * of sequence b (from 0) is at position lens[b] + offset + i of its cache; a
- * packed prompt is committed with n_accepted[b] = (its tokens) - 1.
+ * packed prompt is committed with n_accepted[b] = (its tokens) - 1.  For a sequence
+ * without tokens that is -1, which qspec_kv_commit leaves as it was and reports like
+ * any count below 0: commit a batch that has such sequences without a workspace (the
+ * prompt calls have reported by then what does not fit).
  * Requires head_dim = 128, h_q a multiple of h_kv, 1 <= batch <= 65535,
  * n_tokens >= 1.  All reads of device-side lengths are checked: a sequence
  * whose cu entries (below 0, decreasing, past n_tokens) or positions do not fit
@@ -513,7 +516,9 @@ qspec_status qspec_workspace_status(void* workspace, void* stream);
 /* Version of this ABI (3: adds QSPEC_GEMM_TEST_STALL, qspec_gemm_w4a8, qspec_cast_bf16,
  * qspec_spec_accept_greedy and qspec_gemm_w4a16_noalloc_status; 4: adds
  * qspec_gemm_w4a4_f32in and qspec_gemm_w4a8_f32in; 5: adds qspec_kv_append,
- * qspec_attn_decode, qspec_attn_workspace_size and qspec_kv_commit). */
+ * qspec_attn_decode, qspec_attn_workspace_size and qspec_kv_commit).  The prompt
+ * path's entry points came later under 5, for nothing that was there changed: a
+ * caller that may meet an older library looks for qspec_call among its exports. */
 #define QSPEC_ABI_VERSION 5
 int32_t qspec_abi_version(void);
 

@@ -445,3 +445,24 @@ def test_one_workspace_for_all_token_counts(qs):
     with pytest.raises(qs.QSpecError) as e:
         qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, _i32([plen]), cu=cu, work=small)
     assert e.value.status == 4
+
+
+def test_prompts_with_an_empty_slot_are_committed(qs):
+    """A batch in which one sequence has no tokens: the prompt calls report nothing, the commit without a workspace
+    advances the others, and a sequence that does not fit is told by the prompt calls."""
+    g = _gen(71)
+    new, h_q, h_kv, l_max = [30, 0, 95], 8, 2, 200
+    cu = _i32([0, 30, 30, 125])
+    qkv = _randn(g, 125, (h_q + 2 * h_kv) * D, dtype=torch.float32)
+    kc, vc = (torch.zeros(3, h_kv, l_max, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    work = torch.zeros(qs.attn_prefill_workspace_size(), dtype=torch.uint8, device="cuda")
+    for old, status in (([0, 7, 20], 0), ([0, 7, 150], BAD_INPUT)):
+        lens = _i32(old)
+        q = qs.qkv_rope_append(qkv, lens, 0, kc, vc, h_q, None, cu=cu, work=work)
+        assert qs.workspace_status(work) == status
+        out = qs.attn_prefill(q, cu, lens, kc, vc, h_q, work=work)
+        assert qs.workspace_status(work) == status
+        fits = [m if o + m <= l_max else 0 for m, o in zip(new, old)]
+        _check(out, fits, old, q, kc, vc, h_q)
+        qs.kv_commit(lens, cu.diff() - 1, l_max)
+        assert lens.tolist() == [o + m for o, m in zip(old, fits)]
