@@ -318,7 +318,9 @@ qspec_status qspec_kv_append(const float* qkv, int64_t ld_qkv, int32_t batch, in
  *  out        fp32, row stride ld_out >= h_q * 128.
  *  workspace  >= qspec_attn_workspace_size(...) bytes, 16-byte aligned, zeroed
  *             before its first use; every call that completes leaves it ready
- *             for the next.  Calls sharing one workspace must not overlap.
+ *             for the next of the same batch * h_kv (for one with more of them, or
+ *             after another kind of call, bytes 256 .. 256 + 4 * batch * h_kv must be
+ *             zeroed again).  Calls sharing one workspace must not overlap.
  * The result does not depend on the order in which the CTAs finish. */
 qspec_status qspec_attn_decode(const float* qkv, int64_t ld_qkv, int32_t batch, int32_t t_new,
                                int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* lens,

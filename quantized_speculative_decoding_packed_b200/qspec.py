@@ -155,7 +155,8 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     """A zero-initialised per-device scratch buffer of at least `nbytes` bytes.
 
     The library leaves it ready for reuse after every call that completes.
-    Calls that run concurrently on different streams need separate buffers.
+    Calls that run concurrently on different streams, or come from different
+    host threads, need separate buffers.
     """
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     cur = _WS_CACHE.get(dev)
@@ -463,7 +464,11 @@ def kv_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch
 def attn_decode(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor,
                 v_cache: torch.Tensor, h_q: int, ctx_max: int, out: torch.Tensor | None = None,
                 work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Decode attention of the new tokens over the shared cache -> fp32 [B*T][H*128]."""
+    """Decode attention of the new tokens over the shared cache -> fp32 [B*T][H*128].
+
+    Without `work` the call takes a buffer of this thread and stream; under capture one of the graph's own, which
+    the graph clears before each call (pass `work`, zeroed once, to capture the kernel alone).
+    """
     _qkv_check(qkv)
     _need(lens, torch.int32, "lens")
     b, h_kv, l_max = _kv_cache_check(k_cache, v_cache)

@@ -466,3 +466,29 @@ def test_prompts_with_an_empty_slot_are_committed(qs):
         _check(out, fits, old, q, kc, vc, h_q)
         qs.kv_commit(lens, cu.diff() - 1, l_max)
         assert lens.tolist() == [o + m for o, m in zip(old, fits)]
+
+
+def test_captured_default_outputs_on_a_forked_stream(qs, fresh):
+    """Two calls at once in a graph, one on a forked stream, with outputs and workspaces of their own; the outputs
+    are dropped and taken anew by a second graph."""
+    new, old, h_q, h_kv = [300, 20], [500, 900], 8, 2
+    runs = [_case(81 + i, new, old, h_q, h_kv) for i in range(2)]
+    want = [qs.attn_prefill(q, cu, lens, kc, vc, h_q) for q, kc, vc, cu, lens in runs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            outs = [qs.attn_prefill(q, cu, lens, kc, vc, h_q, stream=s) for (q, kc, vc, cu, lens), s in zip(runs, (side, None))]
+            main.wait_stream(side)
+            sums = [o.float().sum() for o in outs]
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for o, s, ref in zip(outs, sums, want):
+                assert torch.equal(o, ref) and torch.equal(s, ref.float().sum())
+        del outs, sums, graph
