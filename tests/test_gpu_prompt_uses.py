@@ -492,3 +492,48 @@ def test_captured_default_outputs_on_a_forked_stream(qs, fresh):
             for o, s, ref in zip(outs, sums, want):
                 assert torch.equal(o, ref) and torch.equal(s, ref.float().sum())
         del outs, sums, graph
+
+
+@pytest.mark.parametrize("h_q,h_kv,rows,slots", [(8, 2, 200, 6), (4, 4, 700, 3), (32, 8, 60, 40), (14, 2, 90, 70)])
+def test_one_graph_serves_batches_of_any_shape(qs, h_q, h_kv, rows, slots):
+    """Captured once for so many rows and slots, replayed with other token counts (none at all, one long prompt, single
+    tokens, empty slots), lengths and prefixes, on padded rows that hold NaN and stay as they were."""
+    g = _gen(91)
+    r = torch.Generator().manual_seed(92)
+    l_max, p_max = rows + 900, 1500
+    kc, vc = (_randn(g, slots, h_kv, l_max, D) for _ in range(2))
+    pk, pv = (_randn(g, h_kv, p_max, D) for _ in range(2))
+    q = torch.empty(rows, h_q * D, dtype=torch.bfloat16, device="cuda")
+    cu, lens, plen = _i32([0] * (slots + 1)), _i32([0] * slots), _i32([0])
+    out, behind = torch.empty_like(q), torch.empty_like(q)
+
+    def calls(**kw):
+        qs.attn_prefill(q, cu, lens, kc, vc, h_q, out=out, **kw)
+        qs.attn_prefix(q, lens, 0, kc, vc, h_q, pk, pv, plen, cu=cu, out=behind, **kw)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    few = min(slots, rows)
+    spread = torch.rand(slots, generator=r)
+    shapes = [[0] * slots, [0] * (slots - 1) + [rows], [rows] + [0] * (slots - 1), [1] * few + [0] * (slots - few),
+              [int(x) for x in spread / spread.sum() * rows], [min(3, rows // slots)] * slots]
+    for i, new in enumerate(shapes):
+        old = [int(x) for x in torch.randint(0, l_max - rows + 1, (slots,), generator=r)]
+        p = (0, 1, p_max, 129, 640, 128)[i]
+        n = sum(new)
+        q.copy_(_randn(g, rows, h_q * D, scale=1.5))
+        q[n:] = float("nan")
+        cu.copy_(_i32([sum(new[:b]) for b in range(slots + 1)]))
+        lens.copy_(_i32(old))
+        plen.fill_(p)
+        out.fill_(7)
+        behind.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((out[n:] == 7).all()) and bool((behind[n:] == 7).all())
+        if n:
+            _check(out, new, old, q, kc, vc, h_q)
+            _check(behind, new, old, q, kc, vc, h_q, pk, pv, p)
