@@ -415,6 +415,7 @@ class _StreamBuffers(threading.local):
 
     def __init__(self):
         self.of = {}
+        self.retired = []        # what has become too small, for who asked for it may still use it
 
 
 # attn_decode's own: [buffer, bytes from its start that are zero between calls].  The partial results lie
@@ -540,10 +541,7 @@ def _current_device(t: torch.Tensor) -> int:
     return dev
 
 
-# Default workspaces of the prompt attention.  One that has become too small is kept, for who asked for it
-# may still use it.
-_PROMPT_WS = _StreamBuffers()
-_PROMPT_WS_RETIRED: list = []
+_PROMPT_WS = _StreamBuffers()        # the prompt attention's
 
 
 def _new_prompt_workspace(nbytes: int, dev: int) -> torch.Tensor:
@@ -578,7 +576,7 @@ def _prompt_workspace(nbytes: int, dev: int, stream=None) -> torch.Tensor:
     cur = _PROMPT_WS.of.get(key)
     if cur is None or cur.numel() < nbytes:
         if cur is not None:
-            _PROMPT_WS_RETIRED.append(cur)
+            _PROMPT_WS.retired.append(cur)
             nbytes = max(nbytes, 2 * cur.numel())
         cur = _new_prompt_workspace(nbytes, dev)
         _PROMPT_WS.of[key] = cur

@@ -108,7 +108,6 @@ def fresh(qs, monkeypatch):
     """No default workspace from before; the buffers that the test's own thread gets."""
     buffers = qs._StreamBuffers()
     monkeypatch.setattr(qs, "_PROMPT_WS", buffers)
-    monkeypatch.setattr(qs, "_PROMPT_WS_RETIRED", [])
     return buffers
 
 
@@ -153,6 +152,30 @@ def test_threads_on_one_stream(qs, fresh):
             assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1]), i
 
 
+def test_buffers_of_a_thread_end_with_it(qs, fresh):
+    """Short-lived threads, each of which outgrows a buffer, leave none behind."""
+    plen, h_q, h_kv = 100, 4, 2
+    pk, pv = _prefix(26, h_kv, plen)
+    plen_d = _i32([plen])
+    sets = [_case(27 + i, [1] * n, [9] * n, h_q, h_kv) for i, n in enumerate((4, 400))]
+    want = [qs.attn_prefix(c[0], c[4], 0, c[1], c[2], h_q, pk, pv, plen_d) for c in sets]
+    torch.cuda.synchronize()
+    same, held = [], []
+
+    def run():
+        torch.cuda.set_device(0)
+        got = [qs.attn_prefix(c[0], c[4], 0, c[1], c[2], h_q, pk, pv, plen_d) for c in sets]
+        torch.cuda.synchronize()
+        same.append(all(torch.equal(x, y) for x, y in zip(got, want)))
+
+    for _ in range(6):
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        held.append(torch.cuda.memory_allocated())
+    assert same == [True] * 6 and held == held[:1] * 6
+
+
 def test_default_stream_named_where_another_is_current(qs, fresh):
     q, kc, vc, cu, lens = _case(21, [40, 300], [900, 0], 8, 2)
     want = qs.attn_prefill(q, cu, lens, kc, vc, 8)
@@ -178,8 +201,8 @@ def test_workspace_that_is_outgrown_after_a_capture(qs, fresh):
         out = call(small)
     assert fresh.of[key] is first
     _check(call(big), [1] * 400, [30] * 400, big[0], big[1], big[2], h_q, pk, pv, plen)
-    assert fresh.of[key].numel() > first.numel() and len(qs._PROMPT_WS_RETIRED) == 1
-    assert qs._PROMPT_WS_RETIRED[0] is first
+    assert fresh.of[key].numel() > first.numel() and len(fresh.retired) == 1
+    assert fresh.retired[0] is first
     fill = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
     for _ in range(3):
         out.zero_()
