@@ -444,9 +444,10 @@ enum {
   QSPEC_CALL_QKV_ROPE_APPEND = 0,   /* 25 arguments */
   QSPEC_CALL_ATTN_PREFILL = 1,      /* 16 */
   QSPEC_CALL_ATTN_PREFIX = 2,       /* 21 */
-  /* Added to one of the attention calls: a test hook for the failure path, not for normal use.  Each
-   * CTA's loads first wait, for 10 ms at most, on a barrier that nothing signals, and the CTA gives up
-   * as on a real stall: `out` is left incomplete and the status is QSPEC_ERR_TIMEOUT. */
+  /* Added to one of the attention calls: a test hook for the failure path, not for normal use.  The
+   * barrier of each CTA's first key tile expects one arrival too many, so that the waits for it run out
+   * (1 s) and the CTA gives up as on a real stall, with its copies in flight: `out` is left incomplete
+   * and the status is QSPEC_ERR_TIMEOUT. */
   QSPEC_CALL_TEST_STALL = 0x100
 };
 qspec_status qspec_call(int32_t call, const void* args, int32_t n_args, void* stream);

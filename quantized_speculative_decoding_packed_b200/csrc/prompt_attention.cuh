@@ -69,7 +69,7 @@ struct PromptArgs {
   int n_tok, batch, t_new, offset, h_q, h_kv, group, tpt, l_max, prefix_max, mode;
   int ctas;                    // of the attention's grid
   int parts;                   // > 0: few items (and batch <= 32), each can have so many CTAs of its own
-  uint32_t test_stall_ns;      // test hook (0 = off): the loads first wait so long for what nobody signals
+  uint32_t test_stall;         // test hook (0 = off), 1: the first key tile is never known to have landed
 };
 
 // A split item that ends in a CTA's share: its pieces are those of CTAs first .. this one.
@@ -700,11 +700,7 @@ __device__ __forceinline__ void pa_load(const PromptArgs& a, PaShared& sm, uint3
   const uint32_t leader = elect_one_lane();
   uint32_t ring = 0, qn = 0;
   bool ok = true;
-  if (a.test_stall_ns != 0u) {
-    ok = __all_sync(0xffffffffu, mbar_wait_slow(smem_u32(&sm.drained), 0, abort_flag, nullptr, a.test_stall_ns));
-    if (!ok) atomicOr(status, kDevStopped);
-  }
-  for (uint32_t count = 0; ok; ++count) {
+  for (uint32_t count = 0;; ++count) {
     ok = pa_item_wait(sm, count, status);
     if (!ok) break;
     const PaItem it = sm.items[count % kPaItems];
@@ -1384,7 +1380,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       return 14u;                              // item_empty: loads, products, 8 warps of softmax, 4 of output
     };
     static_assert(offsetof(PaShared, items) == 8 * kPaBarriers && kPaBarriers == 2 * kPaStages + 17 + 2 * kPaItems);
-    for (int k = lane; k < kPaBarriers; k += 32) mbar_init(smem_u32(&sm.kv_full[0]) + 8 * k, count_of(k));
+    for (int k = lane; k < kPaBarriers; k += 32)
+      mbar_init(smem_u32(&sm.kv_full[0]) + 8 * k, count_of(k) + (k == 0 ? a.test_stall : 0u));
     if (lane == 0) sm.abort_flag = 0;
     __syncwarp();
     if (lane == 0) fence_barrier_init();

@@ -509,7 +509,7 @@ qspec_status run_prompt_attention(const uint16_t* q, int64_t ld_q, int64_t n_tok
   const int64_t most_tiles = (static_cast<int64_t>(l_max) + 127) / 128 + (with_prefix ? (static_cast<int64_t>(prefix_max) + 127) / 128 : 0);
   const bool unsplit = a.parts > 0 && (most_tiles <= kPaMinPart || (a.parts == 1 && most_tiles <= kPaPartTiles));
   a.ctas = grid;
-  a.test_stall_ns = test_stall ? 10u * 1000u * 1000u : 0u;   // 10 ms
+  a.test_stall = test_stall ? 1u : 0u;
   CUtensorMap tq, tk, tv, tpk, tpv;
   const cuuint64_t q_dims[3] = {kHeadDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(n_tok)};
   const cuuint64_t q_strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld_q) * 2};

@@ -43,7 +43,7 @@ HEAD_DIM = 128           # the KV-cache calls' head dimension
 ROPE_INTERLEAVED, ROPE_Q_FP32 = 1, 2
 GEMM_WEIGHTS_READY = 1   # flag: wq/ws are not written by work still in flight
 GEMM_TEST_STALL = 0x100  # test hook: the GEMM's first wait runs out (QSPEC_GEMM_TEST_STALL)
-CALL_TEST_STALL = 0x100  # test hook: the prompt attention's first wait runs out (QSPEC_CALL_TEST_STALL)
+CALL_TEST_STALL = 0x100  # test hook: the prompt attention's waits run out (QSPEC_CALL_TEST_STALL)
 GEMM_FUSED_QUANT = 0x2   # drafting modes, m <= 32: activations quantized inside the GEMM kernel
 
 

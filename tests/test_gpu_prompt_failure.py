@@ -1,9 +1,9 @@
 """The prompt attention's failure path, made to run on purpose without faulting the GPU.
 
-QSPEC_CALL_TEST_STALL makes each CTA's first wait for its loads one that nothing completes, with a 10 ms
-limit: the CTA gives up (abort flag, status word, drained copies and products, freed tensor memory) and
-returns, the joining kernel runs on what there is, the status reads QSPEC_ERR_TIMEOUT, and the next calls on
-the same workspace are as ever.
+QSPEC_CALL_TEST_STALL gives the barrier of each CTA's first key tile one arrival too many to wait for: the
+waits run out after their second, the CTA gives up (abort flag, status word, drained copies and products,
+freed tensor memory) and returns, the joining kernel runs on what there is, the status reads
+QSPEC_ERR_TIMEOUT, and the next calls on the same workspace are as ever.
 """
 import pytest
 import torch
