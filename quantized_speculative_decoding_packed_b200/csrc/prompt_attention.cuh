@@ -7,9 +7,9 @@
 // cores, the running maximum m and sum l of the softmax in fp32 registers,
 // P = exp(S - m) rounded to bf16 (its only rounding; the values are bf16, and
 // both operands of the product have one type), O += P V in fp32 tensor
-// memory, out = O / l.  m is only raised, and O scaled, when a tile exceeds it
-// by more than 2^kRaise: until then P is at most 2^kRaise, with the same
-// relative rounding.
+// memory, out = O / l (the running maximum and sum: Milakov and Gimelshein,
+// 2018).  m is only raised, and O scaled, when a tile exceeds it by more than
+// 2^kRaise: until then P is at most 2^kRaise, with the same relative rounding.
 //
 // A CTA per SM works through its share of the items (prompt_schedule.cuh).
 //   warp 10: finds the share's items and passes them on (ring of 4);
@@ -25,12 +25,13 @@
 // A piece of a split item is left in the workspace as (m, l, O); a second
 // kernel joins the pieces in order.
 //
-// What bounds it.  Long prompts (8192 tokens, 32 heads over 8: 0.49-0.55 ms, 1.0-1.1 PFLOP/s, at 990 W with the
-// clock at 1.65 GHz): a slot's chain of S (515 cycles), softmax (1600), P V (515) and their hand-overs, about
-// 3300 cycles for a key tile of which the tensor cores work 2060 for both slots.  Single tokens: HBM,
-// and the same chain.  Short prompts: the way to the first item (about 5 us) and HBM's answer to all CTAs'
-// first loads.  Measured and not kept, being slower or no faster: two threads for each row, one pass over S with
-// the maximum kept as a whole number, a third query tile, a fifth key tile, joining in this kernel.
+// What bounds it.  Long prompts (8192 tokens, 32 heads over 8: 506 us, 1.09 PFLOP/s in a burst; 571 us, 0.96
+// in runs of a second, the power limit holding the clock at 1.7 GHz): a slot's chain of S (515 cycles),
+// softmax (1600), P V (515) and their hand-overs, about 3300 cycles for a key tile of which the tensor cores
+// work 2060 for both slots.  Single tokens: HBM, and the same chain.  Short prompts: the way to the first item
+// (about 5 us) and HBM's answer to all CTAs' first loads.  Measured and not kept, being slower or no faster: two
+// threads for each row, one pass over S with the maximum kept as a whole number, a third query tile, a fifth
+// key tile, joining in this kernel.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -225,9 +226,9 @@ __device__ __forceinline__ float max3_nan(float x, float y, float z) {
 // by the share of pairs: none 1400, an eighth 1200, a quarter 1060, three eighths 1190, half 1550.
 constexpr int kPolyEach = 4;
 
-// 2^x for x <= 2^7 without the special function unit: x = k + r with k the nearest
-// integer (by adding 1.5 x 2^23, whose last bits then hold k), 2^r by a
-// polynomial, k added to its exponent.  The polynomial is the one of degree 3
+// 2^x for x <= 2^7 without the special function unit (the reduction of Cody and
+// Waite, 1980): x = k + r with k the nearest integer (by adding 1.5 x 2^23, whose
+// last bits then hold k), 2^r by a polynomial, k added to its exponent.  The polynomial is the one of degree 3
 // with the least relative error on |r| <= 1/2 (7.5e-5, from a weighted
 // least-squares fit): 1/26 of half a step of the bf16 that its result becomes.
 // x <= -126 (a key that is not seen has -inf) is taken as -126, whose power by the cubic, 0.99996 2^-126, is

@@ -12,7 +12,7 @@
 // 512-byte load per row), so the norm is one shuffle reduction and the
 // partner column of a split pair comes from another lane at the same
 // place within its four; up to kRopeHeads rows of a warp are in flight.
-// 4900 tokens of 80 heads (302 MB): 57 us, 5.3 TB/s; with
+// 4900 tokens of 80 heads (302 MB): 58 us, 5.2 TB/s; with
 // a resident grid that goes through the tokens 85-90 (its warps wait for the
 // small loads in turn, where new CTAs have them under way).
 #pragma once
