@@ -448,6 +448,13 @@ def _attn_workspace(nbytes: int, dev: int, counters: int, stream=None) -> torch.
     return ws
 
 
+def attn_workspace(device=None, stream=None) -> torch.Tensor:
+    """The buffer that attn_decode of this thread takes where `work` is not given, on one stream: workspace_status
+    of it tells what the calls have reported.  (A captured call has one of the graph's: pass it `work`.)"""
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    return _attn_workspace(256, torch.cuda.current_device() if dev is None else dev, 0, stream)
+
+
 def kv_append(qkv: torch.Tensor, lens: torch.Tensor, offset: int, k_cache: torch.Tensor,
               v_cache: torch.Tensor, h_q: int, work: torch.Tensor | None = None, stream=None):
     """Write the new tokens' keys and values (rows b*T + t of the fused QKV output)

@@ -143,3 +143,21 @@ def test_status_of_a_stopped_attention_clears_its_word_alone(qs):
         assert qs.workspace_status(buffer[:need]) == status
         assert not buffer[:4].any() and bool((buffer[4:] == 7).all())
         assert qs.workspace_status(buffer[:need]) == 0
+
+
+def test_status_of_the_default_workspace(qs, fresh):
+    """What attn_decode reports without `work` can be read, on the stream and thread of the call."""
+    qkv, lens, k, v, h, ctx = a = _inputs(50, 3, 2, 300)
+    want = _own(qs, a)
+    bad = (qkv, lens - 400, k, v, h, ctx)
+    assert qs.workspace_status(qs.attn_workspace()) == 0
+    _call(qs, bad)
+    assert qs.workspace_status(qs.attn_workspace("cuda")) == 6 and qs.workspace_status(qs.attn_workspace()) == 0
+    assert torch.equal(_call(qs, a), want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _call(qs, bad, stream=side)
+    side.synchronize()
+    assert qs.workspace_status(qs.attn_workspace()) == 0
+    assert qs.workspace_status(qs.attn_workspace(stream=side), stream=side) == 6
+    assert torch.equal(_call(qs, a), want) and qs.workspace_status(qs.attn_workspace(k.device)) == 0
